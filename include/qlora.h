@@ -405,6 +405,136 @@ int qlora_outlier_backward(const qlora_layer_desc* d, int M, const void* X, cons
                            const float* xA, void* dX, float* dA, float* dB, float* dbias,
                            void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Activation and residual in the epilogues, and activations kept in 8 bits
+ * for the backward pass ("Introduce QLoRA-like technique": the fine-tuned
+ * blocks are Dense layers with activations and skip connections between them;
+ * keras-llm-light, "Block-wise gradient checkpointing": activations, not
+ * weights, fill the memory of a fine-tuning step).  The pages give no formula
+ * for either; the library's reading:
+ *
+ *   forward    Z = (Xq Wq^T) sx sw + bias + c (X A) B     (the layer, fp32)
+ *              Y = act(Z) + residual                      (rounded once)
+ *   backward   dX = (dY (Wq sw)^T + c G A^T) * act'(z) + add
+ *
+ * act is the activation that follows the layer (forward), or the one that
+ * produced the layer's input X from z (backward); z is read from its 8-bit
+ * checkpoint.  `add` is a gradient that reaches X by another path, a skip
+ * connection's.
+ *   RELU max(z, 0); GELU z P(z), P the normal distribution function;
+ *   GELU_TANH 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)));
+ *   SILU z / (1 + exp(-z)).
+ * (RELU's slope is 1 where the stored z is positive: a positive z below half a
+ * step of its block is stored as 0 and gets slope 0.  qlora_gemm_dx_relu gates
+ * by the ReLU's own output instead.)
+ *
+ * 8-bit checkpoints.  A layer's input is kept as the codes that the forward
+ * makes anyway, Xq [M,K] and sx [M]: X is read back as Xq * sx.  Any other
+ * activation T [rows, cols] is kept in blocks of 32 consecutive columns of a
+ * row: q [rows, cols] int8 and scales [ceil(cols/32)][rows] fp32 (block-major:
+ * scales[b * rows + row]), scale = amax / 127, q = clamp(rne(v * (127 /
+ * amax)), -127, 127) in fp32, one rounding per operation; blocks with amax <
+ * 2^-100 are stored as zeros with scale 0, and a block that holds an infinity
+ * or a NaN gets codes 0 and scale NaN, so that all of it reads back as NaN.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+    QLORA_ACT_NONE = 0,
+    QLORA_ACT_RELU = 1,
+    QLORA_ACT_GELU = 2,
+    QLORA_ACT_GELU_TANH = 3,
+    QLORA_ACT_SILU = 4
+} qlora_activation;
+
+/* Epilogue of a forward GEMM (host struct of device pointers).  residual
+ * [M,N] act_dtype, 16-byte aligned, or NULL; it may be Y itself (in place).
+ * zq [M,N] int8 (16-byte aligned) and zs [ceil(N/32)][M] fp32 receive the 8-bit
+ * checkpoint of Z; both, or both NULL. */
+typedef struct {
+    qlora_activation act;
+    const void* residual;
+    int8_t* zq;
+    float* zs;
+} qlora_fwd_epilogue;
+
+/* Epilogue of a dX GEMM.  zq [M,K] (16-byte aligned) and zs [ceil(K/32)][M]:
+ * the checkpoint of the z whose activation is X; read unless act is NONE.
+ * add [M,K] act_dtype, 16-byte aligned, or NULL; it may be dX itself. */
+typedef struct {
+    qlora_activation act;
+    const int8_t* zq;
+    const float* zs;
+    const void* add;
+} qlora_dx_epilogue;
+
+/* a2 with activation and residual: qlora_gemm_forward's Z, then the epilogue
+ * above.  With act NONE and no residual or checkpoint it is
+ * qlora_gemm_forward. */
+int qlora_gemm_forward_act(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx,
+                           const int8_t* Wq, const float* sw, const float* bias, const float* xA,
+                           const float* B, const qlora_fwd_epilogue* epilogue, void* Y, void* stream);
+/* The same on packed int4 codes (qlora_gemm_forward_int4). */
+int qlora_gemm_forward_act_int4(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx,
+                                const uint8_t* Wp, const float* sw, const float* bias, const float* xA,
+                                const float* B, const qlora_fwd_epilogue* epilogue, void* Y, void* stream);
+
+/* qlora_quantize_input into the caller's Xq [M,K] (16-byte aligned), sx [M]
+ * and xA [M,r], then qlora_gemm_forward_act.  Xq, sx and xA are the layer's
+ * checkpoint for qlora_backward_ckpt: nothing else of the forward has to be
+ * kept.  No workspace. */
+int qlora_forward_act(const qlora_layer_desc* d, int M, const void* X, const int8_t* Wq, const float* sw,
+                      const float* bias, const float* A, const float* B, const qlora_fwd_epilogue* epilogue,
+                      void* Y, int8_t* Xq, float* sx, float* xA, void* stream);
+
+/* a4 with act'(z) and an added gradient: dX = (dY (Wq * sw)^T + c G A^T) *
+ * act'(z) + add, G from the workspace that a3 filled, as qlora_gemm_dx. */
+int qlora_gemm_dx_act(const qlora_layer_desc* d, int M, const void* dY, const int8_t* Wq, const float* sw,
+                      const float* A, const qlora_dx_epilogue* epilogue, void* dX, const void* workspace,
+                      size_t workspace_bytes, void* stream);
+/* The same on packed int4 codes (qlora_gemm_dx_int4). */
+int qlora_gemm_dx_act_int4(const qlora_layer_desc* d, int M, const void* dY, const uint8_t* Wp, const float* sw,
+                           const float* A, const qlora_dx_epilogue* epilogue, void* dX, const void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Scales of a rows x cols checkpoint: rows * ceil(cols / 32) (0 for a
+ * negative rows or cols < 1). */
+size_t qlora_ckpt_scales(int rows, int cols);
+
+/* Bytes of workspace of qlora_backward_ckpt and qlora_lora_grad_x_ckpt: what
+ * qlora_workspace_bytes gives, at the same place, and the X pass's digits of
+ * sx G.  0 for an invalid descriptor or M > 1047552. */
+size_t qlora_ckpt_workspace_bytes(const qlora_layer_desc* d, int M);
+
+/* a5 from the kept codes: dA = c * (Xq sx)^T G [K,r], G from the workspace
+ * that a3 filled; overwrites the workspace behind qlora_workspace_bytes.  The
+ * sum over the rows runs in integers (sx G as a 31-bit fixed-point value per
+ * column of G): dA does not depend on how it is split.  A column of G that
+ * holds an infinity or a NaN gives NaN in that column of dA.  At most 1047552
+ * rows (QLORA_EUNSUPPORTED). */
+int qlora_lora_grad_x_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx, float* dA,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* The backward of a layer whose forward kept Xq, sx and xA: qlora_lora_grad_dy,
+ * qlora_gemm_dx_act (dX NULL: left out; epilogue NULL: no activation, nothing
+ * added) and qlora_lora_grad_x_ckpt.  In bf16 the factors B and xA of the dY
+ * pass enter at 24 bits for r <= 32 (16 in qlora_backward and for larger r).
+ * Workspace of qlora_ckpt_workspace_bytes; streams, capture and the second
+ * stream from 512 tokens as qlora_backward.  Deterministic. */
+int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx, const void* dY,
+                        const int8_t* Wq, const float* sw, const float* A, const float* B, const float* xA,
+                        const qlora_dx_epilogue* epilogue, void* dX, float* dA, float* dB, float* dbias,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* T [rows, cols] (dtype; 16-byte aligned) -> its 8-bit checkpoint q [rows, cols]
+ * (16-byte aligned), scales [ceil(cols/32)][rows].  Bit-exact with the reading
+ * above.  rows == 0 is a no-op. */
+int qlora_ckpt_save(const void* T, int rows, int cols, qlora_dtype dtype, int8_t* q, float* scales, void* stream);
+
+/* T = q * scale, the product rounded to fp32 and then to `dtype`.  block 32:
+ * scales [ceil(cols/32)][rows]; block 0: one scale per row, scales [rows] (a
+ * layer input's Xq and sx). */
+int qlora_ckpt_load(const int8_t* q, const float* scales, int rows, int cols, int block, qlora_dtype dtype, void* T,
+                    void* stream);
+
 /*
  * Lossy merge ("Introduce QLoRA-like technique", Results footnote: merging
  * LoRA weights into int8 kernels is lossy; "How to fine-tune the 4-bit

@@ -31,11 +31,21 @@ struct FwdEpilogue {
     void* Y;            // [M,N] act
     int32_t* acc;       // [M,N] debug copy or null
     int relu;           // 1: Y = max(Y, 0) (the ReLU that follows the layer in an MLP)
+    // Y = act(Z) + res, Z kept in 8 bits: read only by the kernels' EX forms
+    bool ex = false;
+    int act = 0;               // ActFn (act_epilogue.cuh)
+    const void* res = nullptr; // [M,N] act or null; may be Y itself
+    int8_t* zq = nullptr;      // [M,N] codes of Z or null
+    float* zs = nullptr;       // [ceil(N/32)][M] scales of Z's blocks of 32 columns
 };
 // Y = (Xq Wq^T) sx sw + bias + c xA B with the tcgen05 int8 GEMM.
 // w4: Wq holds packed int4 codes [N, K/2] (K % 32 == 0), expanded in shared memory.
 cudaError_t launch_gemm_i8_fwd(Act act, const int8_t* Xq, const int8_t* Wq, int M, int N, int K,
                                const FwdEpilogue& ep, int* status, cudaStream_t s, bool w4 = false);
+
+// Its large-tile kernels with the EX epilogue (k2_gemm_i8_act.cu).
+cudaError_t launch_gemm_i8_fwd_act(Act act, const int8_t* Xq, const int8_t* Wq, int M, int N, int K,
+                                   const FwdEpilogue& ep, int* status, cudaStream_t s, bool w4);
 
 // The forward GEMM on CTA pairs (256 x 256 tiles, k2_gemm_i8_pair.cu): bf16
 // outputs, rank <= 16, at least one wave of pair tiles.
@@ -69,6 +79,12 @@ struct DxEpilogue {
     int a_js = 1;
     const float* bias = nullptr;      // [K] added per output column, or null
     OutlierArgs ol{};  // ol.par != nullptr: outlier-compensated codes instead of int8 / int4
+    // dX = (.) * act'(z) + add: read only by the kernels' EX forms
+    bool ex = false;
+    int act = 0;               // ActFn (act_epilogue.cuh); 0: no factor, zq not read
+    const int8_t* zq = nullptr;  // [M,K] codes of z
+    const float* zs = nullptr;   // [ceil(K/32)][M] scales of z's blocks of 32 columns
+    const void* add = nullptr;   // [M,K] act or null; may be dX itself
 };
 
 // The one-off quantization of an outlier-compensated int8 kernel W [K,N]
@@ -93,6 +109,10 @@ cudaError_t launch_quantize_outlier(const float* W, int K, int N, const OutlierK
 cudaError_t launch_gemm_dx(Act act, const void* dY, const int8_t* Wq, const float* sw, int M,
                            int N, int K, const DxEpilogue& ep, int* status, cudaStream_t s,
                            bool w4 = false);
+// Its large-tile (tc) or CUDA-core kernels with the EX epilogue (k3_dx_act.cu);
+// mode 0 int8 codes, 1 packed int4.
+cudaError_t launch_gemm_dx_act(Act act, bool tc, const void* dY, const int8_t* Wq, const float* sw, int M, int N,
+                               int K, const DxEpilogue& ep, int* status, cudaStream_t s, int mode);
 // The bf16 dX GEMM on CTA pairs (256 x 256 tiles, k3_dx_pair.cu): for N a
 // multiple of 64, rank <= 16 and at least one wave of pair tiles.
 bool gemm_dx_pair_applies(int M, int N, int K, int r);
@@ -152,10 +172,11 @@ int rank_col_blocks(Act act, int N);
 constexpr int kMaxDirectSlices = 8;
 
 // Pass over dY: G slices into Gp, final dB and dbias.  Gp or dB may be null
-// (that half is skipped); dbias may be null.
+// (that half is skipped); dbias may be null.  precise: with both halves and r
+// <= 32, the tensor-core pass carries the fp32 factors to 24 bits (else 16).
 cudaError_t launch_rank_dy(Act act, const void* dY, const float* B, const float* xA, int M, int N,
                            int r, float c, float* Gp, float* dB, float* dbias, int* status,
-                           cudaStream_t s);
+                           cudaStream_t s, bool precise = false);
 // G [M,r] = the ncb slices of Gp added in ascending order.
 cudaError_t launch_g_reduce(const float* Gp, int ncb, int M, int r, float* G, cudaStream_t s);
 // Pass over X: final dA from X and G given as nsl slices (nsl = 1: G itself).
@@ -166,9 +187,24 @@ cudaError_t launch_rank_x(Act act, const void* X, const float* G, int nsl, int M
 int rank_tc_col_blocks(int C);
 cudaError_t launch_rank_dy_tc(const void* dY, const float* B, const float* xA, int M, int N, int r,
                               float c, float* Gp, float* dB, float* dbias, int* status,
-                              cudaStream_t s);
+                              cudaStream_t s, bool precise = false);
 cudaError_t launch_rank_x_tc(const void* X, const float* G, int nsl, int M, int K, int r, float c,
                              float* dA, int* status, cudaStream_t s);
+
+// dA = c X^T G from the input kept as row codes, X = Xq sx (k4_rank_q.cu): a
+// pass that turns sx G into 8-bit digits in `digits`, then the column sums of
+// Xq on the int8 tensor cores.  M at most kRankQMaxRows.
+constexpr int kRankQMaxRows = 8 * 1023 * 128;
+size_t rank_q_digit_bytes(int M, int r);
+cudaError_t launch_rank_x_q(const int8_t* Xq, const float* sx, const float* G, int nsl, int M, int K, int r,
+                            float c, void* digits, float* dA, int* status, cudaStream_t s);
+
+// ---------------------------------------------------------------- 8-bit checkpoints
+// Blocks of 32 columns of a row: codes q [rows, cols], scales [ceil(cols/32)][rows] (ckpt.cu).
+cudaError_t launch_ckpt_save(Act act, const void* T, int rows, int cols, int8_t* q, float* scales, cudaStream_t s);
+// T = q * scale; block 32, or 0: one scale per row.
+cudaError_t launch_ckpt_load(Act act, const int8_t* q, const float* scales, int rows, int cols, int block, void* T,
+                             cudaStream_t s);
 
 // ---------------------------------------------------------------- KM
 cudaError_t launch_merge_int4(const uint8_t* Wp, const float* sw, const float* A, const float* B,

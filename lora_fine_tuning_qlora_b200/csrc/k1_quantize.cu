@@ -504,34 +504,6 @@ __device__ __forceinline__ void bf16x8_to_f(const uint4 u, float (&f)[8]) {
     }
 }
 
-// Symmetric abs-max codes of 8 values: rne(fl(v * inv)).  The products are
-// rounded to fp32 lane by lane (mul.rn.f32x2: two per instruction, never
-// contracted), converted with round-to-nearest-even (cvt.rni.s32.f32, on the
-// conversion pipe beside the FMA pipe) and packed four to a word with
-// saturation (cvt.pack.sat.s8.s32: |fl(v * inv)| <= 127 * (1 + 2^-24)^2 <
-// 127.5, so saturation is never reached).  Against an fp32 multiply, a
-// 1.5 * 2^23 add and byte permutes on the FMA pipe this ran 72 against 76 us
-// at 16384 x 4096 with the same codes.
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
-    const unsigned long long inv2 = pk2(inv, inv);
-    int c[8];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        unsigned long long prod;
-        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(prod) : "l"(pk2(f[2 * p], f[2 * p + 1])), "l"(inv2));
-        float a, b;
-        unpk2(prod, a, b);
-        asm("cvt.rni.s32.f32 %0, %1;" : "=r"(c[2 * p]) : "f"(a));
-        asm("cvt.rni.s32.f32 %0, %1;" : "=r"(c[2 * p + 1]) : "f"(b));
-    }
-    uint32_t t0, w0, t1, w1;
-    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(t0) : "r"(c[3]), "r"(c[2]), "r"(0));
-    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(w0) : "r"(c[1]), "r"(c[0]), "r"(t0));
-    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(t1) : "r"(c[7]), "r"(c[6]), "r"(0));
-    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(w1) : "r"(c[5]), "r"(c[4]), "r"(t1));
-    return make_uint2(w0, w1);
-}
-
 template <int TPR, int CPT, int RP>
 __global__ void __launch_bounds__(staged::cons<TPR, RP>() + 32, 1)
     k1_quantize_rows_staged_kernel(StagedArgs a, int* status) {

@@ -37,6 +37,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "tile_epilogue.cuh"
+#include "act_epilogue.cuh"
 
 namespace qlora {
 
@@ -45,16 +46,20 @@ namespace {
 constexpr int kQM = 128;             // rows per CTA (256 per pair)
 constexpr int kQN = 256;             // output columns per pair tile (128 of Wq per CTA)
 constexpr int kQK = 128;             // int8 k per stage: one 128-byte swizzle row
-constexpr int kQEpi = 4;             // epilogue warps
+// epilogue warps: one per TMEM lane quarter, or (EX) two, each with half of the
+// tile's columns
+template <bool W4, bool EX>
+__host__ __device__ constexpr int q_epi() { return EX && !W4 ? 8 : 4; }
 constexpr int kQUGroups = 5;         // W4: stage groups of expansion warps (one per stage of the ring)
 constexpr int kQUWPG = 2;            // W4: warps per stage group
 constexpr int kQUnpack = kQUGroups * kQUWPG;  // W4: warps that expand the packed codes
-template <bool W4>
-__host__ __device__ constexpr int q_threads() { return 32 * (2 + kQEpi + (W4 ? kQUnpack : 0)); }
+template <bool W4, bool EX>
+__host__ __device__ constexpr int q_threads() { return 32 * (2 + q_epi<W4, EX>() + (W4 ? kQUnpack : 0)); }
 constexpr int kQSmemLimit = 232448;
 
-template <int RP, bool W4>
+template <int RP, bool W4, bool EX>
 struct PairFwdCfg {
+    static constexpr int kQEpi = q_epi<W4, EX>();
     static constexpr int kABytes = kQM * kQK;             // Xq rows of this CTA: 16 KB
     static constexpr int kBBytes = (kQN / 2) * kQK;       // Wq rows of this CTA: 16 KB
     static constexpr int kPBytes = W4 ? (kQN / 2) * kQK / 2 : 0;  // packed codes: 8 KB
@@ -75,12 +80,16 @@ struct PairFwdCfg {
     static constexpr uint32_t kTmemCols = 2 * kAccCols;   // two buffers: all 512 columns
 };
 
-template <int RP, bool W4>
-__global__ void __launch_bounds__(q_threads<W4>(), 1)
+// EX: the epilogue is Y = act(Z) + res with Z kept in 8 bits
+// (act_epilogue.cuh), in steps of 32 columns, the residual's next step
+// loaded a step ahead.
+template <int RP, bool W4, bool EX>
+__global__ void __launch_bounds__(q_threads<W4, EX>(), 1)
     k2_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                            const __grid_constant__ CUtensorMap tmB, int M, int N, int K,
                            FwdEpilogue ep, int* status) {
-    using C = PairFwdCfg<RP, W4>;
+    using C = PairFwdCfg<RP, W4, EX>;
+    constexpr int kQEpi = C::kQEpi;
     constexpr int S = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -257,7 +266,7 @@ __global__ void __launch_bounds__(q_threads<W4>(), 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------ epilogue
-        const int ew = warp - 2;             // 0 .. 3
+        const int ew = warp - 2;             // 0 .. kQEpi - 1
         const int q = warp & 3;              // TMEM lane quarter of this warp
         const int et = threadIdx.x - 64;
         uint8_t* stg = smem + C::kStgOff + ew * 32 * stage_pitch<__nv_bfloat16>();
@@ -291,16 +300,8 @@ __global__ void __launch_bounds__(q_threads<W4>(), 1)
 #pragma unroll
             for (int j = 0; j < RP; ++j)
                 xa[j] = (row_ok && j < ep.r) ? __ldg(ep.xA + static_cast<size_t>(row) * ep.r + j) * ep.c : 0.f;
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * C::kAccCols;
-#pragma unroll 1
-            for (int col = 0; col < kQN; col += kEpiCols) {
-                uint32_t v[kEpiCols];
-                tmem_ld16(tbase + col, v);
-                tmem_ld_wait();
-                float y[kEpiCols];
+            // y = acc sx sw + bias + c xA B of this lane's row, 16 columns from `col`
+            auto finish16 = [&](const uint32_t (&v)[kEpiCols], int col, float* y) {
 #pragma unroll
                 for (int e = 0; e < kEpiCols; ++e) {
                     const int c = col + e;
@@ -317,6 +318,53 @@ __global__ void __launch_bounds__(q_threads<W4>(), 1)
                     }
                     y[e] = acc;
                 }
+            };
+            if constexpr (EX) {
+                constexpr int kCols = kQN / (kQEpi / 4);  // this warp's columns
+                const int c0 = (ew >> 2) * kCols;
+                const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(ep.res);
+                RowPiece<__nv_bfloat16, 32> rp;
+                if (res) rp.load(res, row, row_ok, n0 + c0, N, vec);
+                const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * C::kAccCols;
+#pragma unroll 1
+                for (int col = c0; col < c0 + kCols && n0 + col < N; col += 32) {
+                    uint32_t v0[kEpiCols], v1[kEpiCols];
+                    tmem_ld16(tbase + col, v0);
+                    tmem_ld16(tbase + col + kEpiCols, v1);
+                    tmem_ld_wait();
+                    float z[32];
+                    finish16(v0, col, z);
+                    finish16(v1, col + kEpiCols, z + kEpiCols);
+                    if (ep.zq && row_ok) ckpt_store(z, ep.zq, ep.zs, row, M, n0 + col, N);
+                    act_apply(ep.act, z);
+                    if (res) {
+                        rp.add_to(z);
+                        if (col + 32 < c0 + kCols) rp.load(res, row, row_ok, n0 + col + 32, N, vec);
+                    }
+                    float y[kEpiCols];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int e = 0; e < kEpiCols; ++e) y[e] = z[h * kEpiCols + e];
+                        store_block<__nv_bfloat16>(stg, y, lane, Y, static_cast<size_t>(N), row0, M,
+                                                   n0 + col + h * kEpiCols, N, vec);
+                    }
+                }
+            } else {
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * C::kAccCols;
+#pragma unroll 1
+            for (int col = 0; col < kQN; col += kEpiCols) {
+                uint32_t v[kEpiCols];
+                tmem_ld16(tbase + col, v);
+                tmem_ld_wait();
+                float y[kEpiCols];
+                finish16(v, col, y);
                 if (ep.relu) {
 #pragma unroll
                     for (int e = 0; e < kEpiCols; ++e) y[e] = y[e] > 0.f ? y[e] : 0.f;
@@ -327,6 +375,7 @@ __global__ void __launch_bounds__(q_threads<W4>(), 1)
                             ep.acc[static_cast<size_t>(row) * N + n0 + col + e] = static_cast<int32_t>(v[e]);
                 }
                 store_block<__nv_bfloat16>(stg, y, lane, Y, static_cast<size_t>(N), row0, M, n0 + col, N, vec);
+            }
             }
             tc_fence_before();
             __syncwarp();
@@ -348,11 +397,11 @@ __global__ void __launch_bounds__(q_threads<W4>(), 1)
     }
 }
 
-template <int RP, bool W4>
+template <int RP, bool W4, bool EX>
 cudaError_t launch_fwd_pair_t(const int8_t* Xq, const int8_t* Wq, int M, int N, int K,
                               const FwdEpilogue& ep, int* status, cudaStream_t s) {
-    using C = PairFwdCfg<RP, W4>;
-    auto kern = k2_gemm_i8_pair_kernel<RP, W4>;
+    using C = PairFwdCfg<RP, W4, EX>;
+    auto kern = k2_gemm_i8_pair_kernel<RP, W4, EX>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kTotal);
     if (e != cudaSuccess) return e;
     CUtensorMap ta, tb;
@@ -365,7 +414,7 @@ cudaError_t launch_fwd_pair_t(const int8_t* Xq, const int8_t* Wq, int M, int N, 
         return cudaErrorInvalidValue;
     const int tiles = ((M + 2 * kQM - 1) / (2 * kQM)) * ((N + kQN - 1) / kQN);
     const int pairs = tiles < sm_count() / 2 ? tiles : sm_count() / 2;
-    return launch_kx(kern, dim3(2 * pairs), dim3(q_threads<W4>()), C::kTotal, s, 2, ta, tb, M, N, K, ep,
+    return launch_kx(kern, dim3(2 * pairs), dim3(q_threads<W4, EX>()), C::kTotal, s, 2, ta, tb, M, N, K, ep,
                      status);
 }
 
@@ -377,16 +426,21 @@ bool gemm_fwd_pair_applies(Act act, int M, int N, int K, int r) {
     return tiles >= sm_count() / 2;
 }
 
+template <int RP>
+cudaError_t launch_fwd_pair_r(const int8_t* Xq, const int8_t* Wq, int M, int N, int K,
+                              const FwdEpilogue& ep, int* status, cudaStream_t s, bool w4) {
+    if (ep.ex)
+        return w4 ? launch_fwd_pair_t<RP, true, true>(Xq, Wq, M, N, K, ep, status, s)
+                  : launch_fwd_pair_t<RP, false, true>(Xq, Wq, M, N, K, ep, status, s);
+    return w4 ? launch_fwd_pair_t<RP, true, false>(Xq, Wq, M, N, K, ep, status, s)
+              : launch_fwd_pair_t<RP, false, false>(Xq, Wq, M, N, K, ep, status, s);
+}
+
 cudaError_t launch_gemm_i8_fwd_pair(const int8_t* Xq, const int8_t* Wq, int M, int N, int K,
                                     const FwdEpilogue& ep, int* status, cudaStream_t s, bool w4) {
-    if (ep.r <= 4)
-        return w4 ? launch_fwd_pair_t<4, true>(Xq, Wq, M, N, K, ep, status, s)
-                  : launch_fwd_pair_t<4, false>(Xq, Wq, M, N, K, ep, status, s);
-    if (ep.r <= 8)
-        return w4 ? launch_fwd_pair_t<8, true>(Xq, Wq, M, N, K, ep, status, s)
-                  : launch_fwd_pair_t<8, false>(Xq, Wq, M, N, K, ep, status, s);
-    return w4 ? launch_fwd_pair_t<16, true>(Xq, Wq, M, N, K, ep, status, s)
-              : launch_fwd_pair_t<16, false>(Xq, Wq, M, N, K, ep, status, s);
+    if (ep.r <= 4) return launch_fwd_pair_r<4>(Xq, Wq, M, N, K, ep, status, s, w4);
+    if (ep.r <= 8) return launch_fwd_pair_r<8>(Xq, Wq, M, N, K, ep, status, s, w4);
+    return launch_fwd_pair_r<16>(Xq, Wq, M, N, K, ep, status, s, w4);
 }
 
 }  // namespace qlora

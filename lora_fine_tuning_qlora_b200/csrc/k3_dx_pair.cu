@@ -34,6 +34,7 @@
 #include "ptx.cuh"
 #include "tile_epilogue.cuh"
 #include "dx_common.cuh"
+#include "act_epilogue.cuh"
 
 namespace qlora {
 
@@ -79,7 +80,9 @@ struct PairCfg {
 // MODE: 0 int8 codes with a scale per contraction row; 1 packed int4 codes;
 // 2 outlier-compensated uint8 affine codes (ep.ol) with their fp16 outliers
 // written over the de-quantized tile.
-template <int RP, int MODE>
+// EX: dX = (.) * act'(z) + add (act_epilogue.cuh), the codes of z, their
+// scales and the added gradient loaded a step of 16 columns ahead.
+template <int RP, int MODE, bool EX>
 __global__ void __launch_bounds__(kPThreads, 1)
     k3_dx_pair_kernel(const __grid_constant__ CUtensorMap tmDY, const int8_t* __restrict__ Wq,
                       const float* __restrict__ sw, int M, int N, int K, DxEpilogue ep,
@@ -367,6 +370,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             float gr[RP];
 #pragma unroll
             for (int j = 0; j < RP; ++j) gr[j] = (row_ok && j < ep.r) ? g_row(ep, M, row, j) * ep.c : 0.f;
+            DxPiece<__nv_bfloat16> px;
+            if constexpr (EX) px.load(ep, M, K, row, row_ok, k0, true);
             const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
             if (!ok) break;
             tc_fence_after();
@@ -391,7 +396,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     }
                     y[e] = acc;
                 }
-                if (ep.gate && row_ok && k0 + col < K) {
+                if constexpr (EX) {
+                    px.apply(ep, y);
+                    if (col + kEpiCols < kPN) px.load(ep, M, K, row, row_ok, k0 + col + kEpiCols, true);
+                }
+                if (!EX && ep.gate && row_ok && k0 + col < K) {
                     // backward of the ReLU that produced this layer's input
                     const uint4* gp = reinterpret_cast<const uint4*>(
                         static_cast<const __nv_bfloat16*>(ep.gate) + static_cast<size_t>(row) * K + k0 + col);
@@ -427,11 +436,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
 }
 
-template <int RP, int MODE>
+template <int RP, int MODE, bool EX>
 cudaError_t launch_pair_t(const void* dY, const int8_t* Wq, const float* sw, int M, int N, int K,
                           const DxEpilogue& ep, int* status, cudaStream_t s) {
     using C = PairCfg<RP>;
-    auto kern = k3_dx_pair_kernel<RP, MODE>;
+    auto kern = k3_dx_pair_kernel<RP, MODE, EX>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kTotal);
     if (e != cudaSuccess) return e;
     // dY as [row][64-column block][64]: one box of 128 rows x one block per stage
@@ -459,19 +468,22 @@ bool gemm_dx_pair_applies(int M, int N, int K, int r) {
     return tiles >= sm_count() / 4;
 }
 
-template <int MODE>
+template <int MODE, bool EX>
 cudaError_t launch_pair_mode(const void* dY, const int8_t* Wq, const float* sw, int M, int N,
                              int K, const DxEpilogue& ep, int* status, cudaStream_t s) {
-    if (ep.r <= 4) return launch_pair_t<4, MODE>(dY, Wq, sw, M, N, K, ep, status, s);
-    if (ep.r <= 8) return launch_pair_t<8, MODE>(dY, Wq, sw, M, N, K, ep, status, s);
-    return launch_pair_t<16, MODE>(dY, Wq, sw, M, N, K, ep, status, s);
+    if (ep.r <= 4) return launch_pair_t<4, MODE, EX>(dY, Wq, sw, M, N, K, ep, status, s);
+    if (ep.r <= 8) return launch_pair_t<8, MODE, EX>(dY, Wq, sw, M, N, K, ep, status, s);
+    return launch_pair_t<16, MODE, EX>(dY, Wq, sw, M, N, K, ep, status, s);
 }
 
 cudaError_t launch_gemm_dx_pair(const void* dY, const int8_t* Wq, const float* sw, int M, int N,
                                 int K, const DxEpilogue& ep, int* status, cudaStream_t s, bool w4) {
-    if (ep.ol.par) return launch_pair_mode<2>(dY, Wq, sw, M, N, K, ep, status, s);
-    return w4 ? launch_pair_mode<1>(dY, Wq, sw, M, N, K, ep, status, s)
-              : launch_pair_mode<0>(dY, Wq, sw, M, N, K, ep, status, s);
+    if (ep.ol.par) return launch_pair_mode<2, false>(dY, Wq, sw, M, N, K, ep, status, s);
+    if (ep.ex)
+        return w4 ? launch_pair_mode<1, true>(dY, Wq, sw, M, N, K, ep, status, s)
+                  : launch_pair_mode<0, true>(dY, Wq, sw, M, N, K, ep, status, s);
+    return w4 ? launch_pair_mode<1, false>(dY, Wq, sw, M, N, K, ep, status, s)
+              : launch_pair_mode<0, false>(dY, Wq, sw, M, N, K, ep, status, s);
 }
 
 }  // namespace qlora

@@ -1,0 +1,347 @@
+// k4_rank_q.cu -- the LoRA gradient of A from an input that the forward kept
+// as its row codes (Xq [M,K] int8, sx [M]):
+//
+//   dA[k,j] = c sum_m (Xq[m,k] sx[m]) G[m,j] = c sum_m Xq[m,k] V[m,j],
+//   V[m,j]  = sx[m] G[m,j]
+//
+// ("Parameter-efficient fine-tuning of GPT-2 with LoRA", "LoRA equation", for
+// the product; the kept codes are those of the forward's input quantizer.)
+// The row scale moves to the skinny factor, so the wide operand stays the
+// codes as they lie in memory and the sum runs on tcgen05.mma.kind::i8 with
+// exact int32 accumulation: V is written as four signed 8-bit digits of a
+// fixed-point value per column,
+//   V[m,j] 2^p_j = d0 + 2^8 d1 + 2^16 d2 + 2^24 d3,  |V 2^p| <= 2^30,
+// p_j from the column's largest magnitude, so a digit's sums over the rows
+// are integers and dA is the same bits whatever the order or the split (the
+// only roundings: V to 31 bits below its column's maximum, and the result).
+//
+// Bound by reading the codes once: M K bytes, half of a bf16 input.  The
+// codes need no conversion on the way: a TMA box of 128 rows x 128 columns
+// (128-byte swizzle) is the MN-major A operand (M = 128 columns, K = 32 rows
+// per MMA) as it lands.  The digits of a 128-row tile are prepared once by
+// the digit kernel in the K-major table layout the MMA reads, so every CTA
+// only copies 512 ceil4(r) bytes of them beside each 16 KB tile.
+//
+// Rows are split over a cluster of CL <= 8 CTAs per 128-column block, whose
+// partial sums meet in the shared memory of the CTA that owns the column, as
+// int64.  Warps: 0 producer, 1 TMEM owner and MMA issuer, 2..5 read-out.
+#include "internal.h"
+#include "ptx.cuh"
+#include "tile_epilogue.cuh"
+
+namespace qlora {
+
+namespace {
+
+constexpr int kRows = 128;                        // rows of a tile (contraction)
+constexpr int kCols = 128;                        // columns of a tile: one swizzle row of codes
+constexpr uint32_t kTileBytes = kRows * kCols;
+constexpr uint32_t kSbo = (kRows / 16) * 128;     // 8-row group stride of a digit table
+constexpr int kThreads = 32 * 6;
+constexpr int kMaxCl = 8;
+constexpr int kMaxTilesPerCta = 1023;             // 1023 * 128 * 128 * 128 < 2^31
+constexpr int kMaxStages = 8;
+constexpr int kPrepThreads = 1024;
+
+__host__ __device__ constexpr int ceil4(int r) { return (r + 3) / 4 * 4; }
+
+// digits buffer: int p[64] (the columns' exponents), then the tables [tile][4 ceil4(r)][128]
+constexpr uint32_t kExpBytes = 256;
+constexpr int kExpNaN = -0x40000000;  // the column holds an infinity or a NaN
+
+// Byte offset of digit row n (= digit * ceil4(r) + j) of tile row k.
+__device__ __forceinline__ uint32_t digit_off(int n, int k) {
+    return static_cast<uint32_t>((n >> 3) * kSbo + (k >> 4) * 128 + (n & 7) * 16 + (k & 15));
+}
+
+// One cluster.  Two sweeps over G: the columns' maxima of |V|, then the
+// digits.  (Latency-bound: at 16384 rows and rank 4 each of the 8192 threads
+// takes 8 elements; beside the dX GEMM it is hidden.)
+__global__ void __launch_bounds__(kPrepThreads) k4_q_digits_kernel(const float* __restrict__ G, int nsl,
+                                                                   const float* __restrict__ sx, int M, int r,
+                                                                   uint8_t* __restrict__ digits) {
+    __shared__ uint32_t top[64];
+    __shared__ int pexp[64];
+    const uint32_t rank = cluster_ctarank();
+    uint32_t CL;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(CL));
+    const int tid = threadIdx.x;
+    const size_t n = static_cast<size_t>(M) * r;
+    const size_t step = static_cast<size_t>(CL) * kPrepThreads;
+    pdl_trigger();
+    if (tid < 64) top[tid] = 0u;
+    __syncthreads();
+    pdl_wait();
+    auto value = [&](size_t m, int j) {
+        return sum_slices(G + m * r + j, n, nsl) * __ldg(sx + m);
+    };
+    for (size_t i = rank * kPrepThreads + tid; i < n; i += step) {
+        const size_t m = i / r;
+        const int j = static_cast<int>(i - m * r);
+        atomicMax(&top[j], __float_as_uint(value(m, j)) & 0x7FFFFFFFu);
+    }
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    if (tid < 64) {
+        uint32_t t = 0;
+        for (uint32_t q = 0; q < CL; ++q) t = max(t, dsmem_ld_u32(dsmem_addr(&top[tid], q)));
+        // t < 2^(E - 126) for a biased exponent E, so V 2^(156 - E) < 2^30
+        const int E = static_cast<int>(t >> 23);
+        const int p = t >= 0x7F800000u ? kExpNaN : (t == 0u ? 0 : 156 - (E > 0 ? E : 1));
+        pexp[tid] = p;
+        if (rank == 0) reinterpret_cast<int*>(digits)[tid] = p;
+    }
+    __syncthreads();
+    const int RP = ceil4(r);
+    const int tiles = (M + kRows - 1) / kRows;
+    const size_t items = static_cast<size_t>(tiles) * RP * (kRows / 4);
+    for (size_t i = rank * kPrepThreads + tid; i < items; i += step) {
+        const int j = static_cast<int>(i % RP);
+        const size_t rest = i / RP;
+        const int g = static_cast<int>(rest % (kRows / 4));
+        const size_t tile = rest / (kRows / 4);
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        const int p = j < r ? pexp[j] : kExpNaN;
+        if (p != kExpNaN) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const size_t m = tile * kRows + 4 * g + e;
+                if (m >= static_cast<size_t>(M)) continue;
+                int t = __float2int_rn(scalbnf(value(m, j), p));
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const int c = d < 3 ? static_cast<int>(static_cast<int8_t>(t & 0xFF)) : t;
+                    w[d] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * e);
+                    t = (t - c) >> 8;
+                }
+            }
+        }
+        uint8_t* tab = digits + kExpBytes + tile * (static_cast<size_t>(4 * RP) * kRows);
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            *reinterpret_cast<uint32_t*>(tab + digit_off(d * RP + j, 4 * g)) = w[d];
+    }
+    // no CTA leaves while another reads its maxima
+    cluster_arrive();
+    cluster_wait();
+}
+
+struct RankQArgs {
+    const uint8_t* digits;
+    float* dA;
+    int M, K, r;
+    int tiles_per_cta;
+    int stages;
+    float c;
+};
+
+struct RqLayout {
+    int RP, NV;
+    uint32_t stage, recv, bar, total, tmem_cols;
+    __host__ __device__ RqLayout(int r, int stages) {
+        RP = ceil4(r);
+        NV = 4 * RP;
+        stage = kTileBytes + static_cast<uint32_t>(NV) * kRows;
+        recv = static_cast<uint32_t>(stages) * stage;
+        bar = recv + static_cast<uint32_t>((kCols + kMaxCl) * r * 8);
+        total = bar + (2 * kMaxStages + 4) * 8;
+        tmem_cols = 32;
+        while (tmem_cols < static_cast<uint32_t>(NV)) tmem_cols <<= 1;
+    }
+};
+
+__global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_constant__ CUtensorMap tmX, RankQArgs a,
+                                                             int* status) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int S = a.stages;
+    const RqLayout L(a.r, S);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bar);
+    uint64_t* empty = full + kMaxStages;
+    uint64_t* dfull = empty + kMaxStages;
+    uint64_t* rbar = dfull + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + 1);
+    // recv[q][c][j]: the sums of CTA q for column cbeg + c of this CTA's slice
+    long long* recv = reinterpret_cast<long long*>(smem + L.recv);
+    uint32_t CL;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(CL));
+    const uint32_t crank = cluster_ctarank();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int col0 = blockIdx.x * kCols;
+    const int mtiles = (a.M + kRows - 1) / kRows;
+    const int t0 = blockIdx.y * a.tiles_per_cta;
+    const int nt = max(0, min(mtiles, t0 + a.tiles_per_cta) - t0);
+    const int per = (kCols + static_cast<int>(CL) - 1) / static_cast<int>(CL);
+    const int cbeg = static_cast<int>(crank) * per;
+    const int cend = min(kCols, cbeg + per);
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(dfull, 1);
+        mbar_init(rbar, static_cast<uint32_t>(static_cast<int>(CL) * max(1, cend - cbeg)));
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, L.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    cluster_arrive_relaxed();  // no CTA arrives on another's barrier before it is initialised
+    pdl_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tmX);
+            const uint32_t tab = static_cast<uint32_t>(L.NV) * kRows;
+            const uint8_t* src = a.digits + kExpBytes;
+            for (int i = 0; i < nt; ++i) {
+                const int s = i % S;
+                if (i >= S && !mbar_wait(&empty[s], ((i / S) - 1) & 1, status)) break;
+                uint8_t* st = smem + s * L.stage;
+                mbar_arrive_expect_tx(&full[s], L.stage);
+                tma_load_2d(st, &tmX, &full[s], col0, (t0 + i) * kRows);
+                bulk_load(st + kTileBytes, src + static_cast<size_t>(t0 + i) * tab, tab, &full[s]);
+            }
+        }
+        __syncwarp();
+        cluster_wait();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t id = idesc_i8_at(kCols, L.NV);
+            bool ok = true;
+            for (int i = 0; i < nt; ++i) {
+                const int s = i % S;
+                if (!mbar_wait(&full[s], (i / S) & 1, status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t xb = smem_u32(smem + s * L.stage);
+                const uint32_t vb = xb + kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < kRows / 32; ++kk) {
+                    // 32 rows: four 8-row swizzle groups of the tile, two 16-byte
+                    // core matrices of the digit table
+                    const uint64_t ad = smem_desc(xb + kk * 4096, kTileBytes, 1024, kLayoutSw128);
+                    const uint64_t bd = smem_desc(vb + kk * 256, 128, kSbo, kLayoutNone);
+                    mma_i8(tmem, ad, bd, id, (i > 0 || kk > 0) ? 1u : 0u);
+                }
+                mma_commit(&empty[s]);
+            }
+            if (ok) mma_commit(dfull);
+        }
+        __syncwarp();
+        cluster_wait();
+    } else {
+        cluster_wait();  // every CTA of the cluster has initialised its barriers
+        const int wq = warp & 3;
+        const int rr = wq * 32 + lane;  // column of the block
+        const int owner = rr / per;
+        const uint32_t dst =
+            dsmem_addr(recv + static_cast<size_t>(static_cast<int>(crank) * per + rr - owner * per) * a.r,
+                       static_cast<uint32_t>(owner));
+        bool ok = nt > 0;
+        if (nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(dfull, 0, status));
+        tc_fence_after();
+        const uint32_t base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+        for (int j0 = 0; j0 < L.RP; j0 += 4) {
+            long long sum[4] = {0, 0, 0, 0};
+            if (ok) {
+                uint32_t d[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld4(base + i * L.RP + j0, d[i]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sum[e] = static_cast<long long>(static_cast<int>(d[0][e])) +
+                             static_cast<long long>(static_cast<int>(d[1][e])) * 256 +
+                             static_cast<long long>(static_cast<int>(d[2][e])) * 65536 +
+                             static_cast<long long>(static_cast<int>(d[3][e])) * 16777216;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j0 + e < a.r) dsmem_st_i64(dst + 8u * static_cast<uint32_t>(j0 + e), sum[e]);
+        }
+        tc_fence_before();
+        mbar_arrive_remote(dsmem_addr(rbar, static_cast<uint32_t>(owner)));
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L.tmem_cols);
+    }
+    // this CTA's slice of the columns; once every partial has arrived nothing
+    // touches this CTA's shared memory from outside
+    const int width = cend - cbeg;
+    if (width > 0 && mbar_wait_cluster(rbar, 0, status)) {
+        const int* pexp = reinterpret_cast<const int*>(a.digits);
+        for (int idx = threadIdx.x; idx < width * a.r; idx += kThreads) {
+            const int cc = idx / a.r, j = idx - cc * a.r;
+            const int col = col0 + cbeg + cc;
+            if (col >= a.K) continue;
+            long long sum = 0;
+            for (int q = 0; q < static_cast<int>(CL); ++q)
+                sum += recv[static_cast<size_t>(q * per + cc) * a.r + j];
+            const int p = __ldg(pexp + j);
+            const double v = p == kExpNaN ? __longlong_as_double(0x7FF8000000000000LL)
+                                          : scalbn(static_cast<double>(sum), -p) * static_cast<double>(a.c);
+            a.dA[static_cast<size_t>(col) * a.r + j] = static_cast<float>(v);
+        }
+    }
+}
+
+}  // namespace
+
+size_t rank_q_digit_bytes(int M, int r) {
+    return kExpBytes + static_cast<size_t>((M + kRows - 1) / kRows) * 4 * ceil4(r) * kRows;
+}
+
+cudaError_t launch_rank_x_q(const int8_t* Xq, const float* sx, const float* G, int nsl, int M, int K, int r,
+                            float c, void* digits, float* dA, int* status, cudaStream_t s) {
+    if (M > kRankQMaxRows) return cudaErrorInvalidValue;
+    // digits: a cluster of CTAs, about 8 elements a thread
+    const size_t n = static_cast<size_t>(M) * r;
+    int pc = 1;
+    while (pc < 8 && n > static_cast<size_t>(pc) * kPrepThreads * 8) pc *= 2;
+    cudaError_t e = launch_k(k4_q_digits_kernel, dim3(1, pc), dim3(kPrepThreads), 0, s, pc, G, nsl, sx, M, r,
+                             static_cast<uint8_t*>(digits));
+    if (e != cudaSuccess) return e;
+    CUtensorMap tm;
+    if (!make_tmap_2d(&tm, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, M, K, K, kRows, kCols, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    RankQArgs a{};
+    a.digits = static_cast<const uint8_t*>(digits);
+    a.dA = dA;
+    a.M = M;
+    a.K = K;
+    a.r = r;
+    a.c = c;
+    const int mtiles = (M + kRows - 1) / kRows;
+    a.tiles_per_cta = (mtiles + kMaxCl - 1) / kMaxCl;
+    const int want = (rank_pass_rows() + kRows - 1) / kRows;  // a caller's minimum rows per CTA
+    if (want > a.tiles_per_cta) a.tiles_per_cta = want;
+    if (a.tiles_per_cta > kMaxTilesPerCta) a.tiles_per_cta = kMaxTilesPerCta;
+    const int cl = (mtiles + a.tiles_per_cta - 1) / a.tiles_per_cta;
+    // two CTAs per SM: about 100 KB each
+    const RqLayout one(r, 1);
+    int S = static_cast<int>((104 * 1024 - (one.total - one.recv)) / static_cast<double>(one.stage));
+    S = S < 2 ? 2 : (S > kMaxStages ? kMaxStages : S);
+    a.stages = S;
+    const RqLayout L(r, S);
+    const size_t smem = L.total + 1024;
+    e = ensure_smem_attr(reinterpret_cast<const void*>(k4_rank_q_kernel), static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_k(k4_rank_q_kernel, dim3((K + kCols - 1) / kCols, cl), dim3(kThreads), smem, s, cl, tm, a, status);
+}
+
+}  // namespace qlora

@@ -15,6 +15,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "tile_epilogue.cuh"
+#include "act_epilogue.cuh"
 
 namespace qlora {
 
@@ -316,10 +317,29 @@ int qlora_quantize_input(const qlora_layer_desc* d, int M, const void* X, const 
                        "input quantizer launch");
 }
 
+// The checks of a forward epilogue and its part of the launch arguments.
+static int forward_epilogue(const qlora_layer_desc* d, const qlora_fwd_epilogue* x, const void* Y, FwdEpilogue& ep) {
+    if (!x) return QLORA_OK;
+    QL_REQUIRE(x->act >= QLORA_ACT_NONE && x->act <= QLORA_ACT_SILU, QLORA_EINVAL, "unknown activation");
+    QL_REQUIRE((x->zq == nullptr) == (x->zs == nullptr), QLORA_EINVAL,
+               "zq and zs go together: both, or neither");
+    QL_REQUIRE(!x->residual || aligned(x->residual, 16), QLORA_EALIGN, "residual must be 16-byte aligned");
+    QL_REQUIRE(!x->zq || (aligned(x->zq, 16) && aligned(x->zs, 4)), QLORA_EALIGN,
+               "zq must be 16-byte aligned, zs 4-byte aligned");
+    QL_REQUIRE(static_cast<const void*>(x->zq) != Y || !x->zq, QLORA_EINVAL, "zq must not alias Y");
+    (void)d;
+    ep.ex = x->act != QLORA_ACT_NONE || x->residual || x->zq;
+    ep.act = static_cast<int>(x->act);
+    ep.res = x->residual;
+    ep.zq = x->zq;
+    ep.zs = x->zs;
+    return QLORA_OK;
+}
+
 static int gemm_forward_impl(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx,
                              const int8_t* Wq, const float* sw, const float* bias,
                              const float* xA, const float* B, void* Y, int32_t* acc, int relu,
-                             void* stream, bool w4 = false) {
+                             void* stream, bool w4 = false, const qlora_fwd_epilogue* x = nullptr) {
     int rc = check_layer(d, M);
     if (rc != QLORA_OK) return rc;
     QL_REQUIRE(!w4 || d->K % 32 == 0, QLORA_EUNSUPPORTED,
@@ -330,10 +350,12 @@ static int gemm_forward_impl(const qlora_layer_desc* d, int M, const int8_t* Xq,
     QL_REQUIRE(aligned(sx, 4) && aligned(sw, 4) && aligned(xA, 4) && aligned(B, 4) &&
                    (!bias || aligned(bias, 4)) && (!acc || aligned(acc, 4)),
                QLORA_EALIGN, "fp32/int32 vectors must be 4-byte aligned");
+    FwdEpilogue ep;
+    rc = forward_epilogue(d, x, Y, ep);
+    if (rc != QLORA_OK) return rc;
     if (M == 0) return QLORA_OK;
     int* status = status_ptr();
     QL_REQUIRE(status, QLORA_ECUDA, "no CUDA device");
-    FwdEpilogue ep;
     ep.sx = sx;
     ep.sw = sw;
     ep.bias = bias;
@@ -361,9 +383,56 @@ int qlora_gemm_forward_relu(const qlora_layer_desc* d, int M, const int8_t* Xq, 
     return gemm_forward_impl(d, M, Xq, sx, Wq, sw, bias, xA, B, Y, acc, 1, stream);
 }
 
+int qlora_gemm_forward_act(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx,
+                           const int8_t* Wq, const float* sw, const float* bias, const float* xA,
+                           const float* B, const qlora_fwd_epilogue* epilogue, void* Y, void* stream) {
+    if (!epilogue) return fail(QLORA_EINVAL, "NULL pointer argument");
+    return gemm_forward_impl(d, M, Xq, sx, Wq, sw, bias, xA, B, Y, nullptr, 0, stream, false, epilogue);
+}
+
+int qlora_gemm_forward_act_int4(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx,
+                                const uint8_t* Wp, const float* sw, const float* bias, const float* xA,
+                                const float* B, const qlora_fwd_epilogue* epilogue, void* Y, void* stream) {
+    if (!epilogue) return fail(QLORA_EINVAL, "NULL pointer argument");
+    return gemm_forward_impl(d, M, Xq, sx, reinterpret_cast<const int8_t*>(Wp), sw, bias, xA, B, Y, nullptr, 0,
+                             stream, true, epilogue);
+}
+
+int qlora_forward_act(const qlora_layer_desc* d, int M, const void* X, const int8_t* Wq, const float* sw,
+                      const float* bias, const float* A, const float* B, const qlora_fwd_epilogue* epilogue,
+                      void* Y, int8_t* Xq, float* sx, float* xA, void* stream) {
+    int rc = check_layer(d, M);
+    if (rc != QLORA_OK) return rc;
+    // everything is checked before the first launch
+    QL_REQUIRE(X && A && Xq && sx && xA && Wq && sw && B && Y && epilogue, QLORA_EINVAL, "NULL pointer argument");
+    QL_REQUIRE(aligned(X, 16) && aligned(Xq, 16) && aligned(Wq, 16) && aligned(Y, 16), QLORA_EALIGN,
+               "X, Xq, Wq and Y must be 16-byte aligned");
+    QL_REQUIRE(aligned(A, 4) && aligned(sx, 4) && aligned(xA, 4) && aligned(sw, 4) && aligned(B, 4) &&
+                   (!bias || aligned(bias, 4)),
+               QLORA_EALIGN, "fp32 vectors must be 4-byte aligned");
+    FwdEpilogue ep;
+    rc = forward_epilogue(d, epilogue, Y, ep);
+    if (rc != QLORA_OK) return rc;
+    rc = qlora_quantize_input(d, M, X, A, Xq, sx, xA, stream);
+    if (rc != QLORA_OK) return rc;
+    return gemm_forward_impl(d, M, Xq, sx, Wq, sw, bias, xA, B, Y, nullptr, 0, stream, false, epilogue);
+}
+
+// The dY pass behind qlora_lora_grad_dy; precise: the fp32 factors to 24 bits
+// (ranks up to 32), for the backward from 8-bit checkpoints.
+static int lora_grad_dy_impl(const qlora_layer_desc* d, int M, const void* dY, const float* B,
+                             const float* xA, float* dB, float* dbias, float* G, void* workspace,
+                             size_t workspace_bytes, void* stream, bool precise);
+
 int qlora_lora_grad_dy(const qlora_layer_desc* d, int M, const void* dY, const float* B,
                        const float* xA, float* dB, float* dbias, float* G, void* workspace,
                        size_t workspace_bytes, void* stream) {
+    return lora_grad_dy_impl(d, M, dY, B, xA, dB, dbias, G, workspace, workspace_bytes, stream, false);
+}
+
+static int lora_grad_dy_impl(const qlora_layer_desc* d, int M, const void* dY, const float* B,
+                             const float* xA, float* dB, float* dbias, float* G, void* workspace,
+                             size_t workspace_bytes, void* stream, bool precise) {
     int rc = check_layer(d, M);
     if (rc != QLORA_OK) return rc;
     QL_REQUIRE(dY && B && xA && dB && workspace, QLORA_EINVAL, "NULL pointer argument");
@@ -385,7 +454,7 @@ int qlora_lora_grad_dy(const qlora_layer_desc* d, int M, const void* dY, const f
     QL_REQUIRE(status, QLORA_ECUDA, "no CUDA device");
     float* gp = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.gp);
     rc = cuda_status(launch_rank_dy(act_of(d), dY, B, xA, M, d->N, d->r, lora_scale(d), gp, dB,
-                                    dbias, status, s),
+                                    dbias, status, s, precise),
                      "dY pass launch");
     if (rc == QLORA_OK && w.reduce)
         rc = cuda_status(launch_g_reduce(gp, w.ncb, M, d->r,
@@ -445,10 +514,27 @@ int qlora_lora_grad_b(const qlora_layer_desc* d, int M, const void* dY, const fl
                        "dB pass launch");
 }
 
+// The checks of a dX epilogue and its part of the launch arguments.
+static int dx_epilogue(const qlora_dx_epilogue* x, DxEpilogue& ep) {
+    if (!x) return QLORA_OK;
+    QL_REQUIRE(x->act >= QLORA_ACT_NONE && x->act <= QLORA_ACT_SILU, QLORA_EINVAL, "unknown activation");
+    QL_REQUIRE(x->act == QLORA_ACT_NONE || (x->zq && x->zs), QLORA_EINVAL,
+               "an activation's gradient needs zq and zs");
+    QL_REQUIRE(x->act == QLORA_ACT_NONE || (aligned(x->zq, 16) && aligned(x->zs, 4)), QLORA_EALIGN,
+               "zq must be 16-byte aligned, zs 4-byte aligned");
+    QL_REQUIRE(!x->add || aligned(x->add, 16), QLORA_EALIGN, "add must be 16-byte aligned");
+    ep.ex = x->act != QLORA_ACT_NONE || x->add;
+    ep.act = static_cast<int>(x->act);
+    ep.zq = x->zq;
+    ep.zs = x->zs;
+    ep.add = x->add;
+    return QLORA_OK;
+}
+
 static int gemm_dx_impl(const qlora_layer_desc* d, int M, const void* dY, const int8_t* Wq,
                         const float* sw, const float* A, const void* gate, void* dX,
                         const void* workspace, size_t workspace_bytes, void* stream,
-                        bool w4 = false) {
+                        bool w4 = false, const qlora_dx_epilogue* x = nullptr) {
     int rc = check_layer(d, M);
     if (rc != QLORA_OK) return rc;
     QL_REQUIRE(!w4 || d->K % 32 == 0, QLORA_EUNSUPPORTED,
@@ -458,12 +544,14 @@ static int gemm_dx_impl(const qlora_layer_desc* d, int M, const void* dY, const 
                QLORA_EALIGN, "dY, Wq and dX must be 16-byte aligned, workspace 256-byte aligned");
     QL_REQUIRE(aligned(sw, 4) && aligned(A, 4), QLORA_EALIGN, "fp32 vectors must be 4-byte aligned");
     QL_REQUIRE(!gate || aligned(gate, 16), QLORA_EALIGN, "X must be 16-byte aligned");
+    DxEpilogue ep;
+    rc = dx_epilogue(x, ep);
+    if (rc != QLORA_OK) return rc;
     if (M == 0) return QLORA_OK;
     const WsLayout w = layout_for(*d, M);
     QL_REQUIRE(workspace_bytes >= w.total, QLORA_EINVAL, "workspace too small");
     int* status = status_ptr();
     QL_REQUIRE(status, QLORA_ECUDA, "no CUDA device");
-    DxEpilogue ep;
     ep.Gp = g_source(w, workspace, &ep.ncb);
     ep.A = A;
     ep.r = d->r;
@@ -486,6 +574,21 @@ int qlora_gemm_dx_relu(const qlora_layer_desc* d, int M, const void* dY, const i
                        const void* workspace, size_t workspace_bytes, void* stream) {
     if (!X) return fail(QLORA_EINVAL, "NULL pointer argument");
     return gemm_dx_impl(d, M, dY, Wq, sw, A, X, dX, workspace, workspace_bytes, stream);
+}
+
+int qlora_gemm_dx_act(const qlora_layer_desc* d, int M, const void* dY, const int8_t* Wq, const float* sw,
+                      const float* A, const qlora_dx_epilogue* epilogue, void* dX, const void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    if (!epilogue) return fail(QLORA_EINVAL, "NULL pointer argument");
+    return gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, epilogue);
+}
+
+int qlora_gemm_dx_act_int4(const qlora_layer_desc* d, int M, const void* dY, const uint8_t* Wp, const float* sw,
+                           const float* A, const qlora_dx_epilogue* epilogue, void* dX, const void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    if (!epilogue) return fail(QLORA_EINVAL, "NULL pointer argument");
+    return gemm_dx_impl(d, M, dY, reinterpret_cast<const int8_t*>(Wp), sw, A, nullptr, dX, workspace, workspace_bytes,
+                        stream, true, epilogue);
 }
 
 int qlora_set_rank_pass_rows(int rows) {
@@ -628,6 +731,131 @@ int qlora_backward(const qlora_layer_desc* d, int M, const void* X, const void* 
         if (rc != QLORA_OK) return rc;
     }
     return qlora_lora_grad_x(d, M, X, dA, workspace, workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit activation checkpoints
+// ---------------------------------------------------------------------------
+size_t qlora_ckpt_scales(int rows, int cols) {
+    if (rows < 0 || cols < 1) return 0;
+    return static_cast<size_t>(rows) * ((static_cast<size_t>(cols) + kCkptBlock - 1) / kCkptBlock);
+}
+
+size_t qlora_ckpt_workspace_bytes(const qlora_layer_desc* d, int M) {
+    if (check_desc(d) != QLORA_OK || M < 0 || M > kRankQMaxRows) return 0;
+    if (M == 0) return 256;
+    return layout_for(*d, M).total + align256(rank_q_digit_bytes(M, d->r));
+}
+
+// Shared by the step-level call and the composite, both of which have
+// checked their arguments.
+static int grad_x_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx, float* dA,
+                       void* workspace, cudaStream_t s) {
+    const WsLayout w = layout_for(*d, M);
+    int* status = status_ptr();
+    QL_REQUIRE(status, QLORA_ECUDA, "no CUDA device");
+    int nsl = 0;
+    const float* g = g_source(w, workspace, &nsl);
+    return cuda_status(launch_rank_x_q(Xq, sx, g, nsl, M, d->K, d->r, lora_scale(d),
+                                       static_cast<uint8_t*>(workspace) + w.total, dA, status, s),
+                       "X pass launch");
+}
+
+int qlora_lora_grad_x_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx, float* dA,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_layer(d, M);
+    if (rc != QLORA_OK) return rc;
+    QL_REQUIRE(Xq && sx && dA && workspace, QLORA_EINVAL, "NULL pointer argument");
+    QL_REQUIRE(aligned(Xq, 16) && aligned(workspace, 256), QLORA_EALIGN,
+               "Xq must be 16-byte aligned, workspace 256-byte aligned");
+    QL_REQUIRE(aligned(sx, 4) && aligned(dA, 4), QLORA_EALIGN, "fp32 vectors must be 4-byte aligned");
+    QL_REQUIRE(M <= kRankQMaxRows, QLORA_EUNSUPPORTED, "more than 1047552 rows would overflow the int32 sums");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (M == 0) return cuda_status(cudaMemsetAsync(dA, 0, sizeof(float) * d->K * d->r, s), "memset dA");
+    QL_REQUIRE(workspace_bytes >= qlora_ckpt_workspace_bytes(d, M), QLORA_EINVAL, "workspace too small");
+    return grad_x_ckpt(d, M, Xq, sx, dA, workspace, s);
+}
+
+int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx, const void* dY,
+                        const int8_t* Wq, const float* sw, const float* A, const float* B, const float* xA,
+                        const qlora_dx_epilogue* epilogue, void* dX, float* dA, float* dB, float* dbias,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_layer(d, M);
+    if (rc != QLORA_OK) return rc;
+    QL_REQUIRE(Xq && sx && dY && Wq && sw && A && B && xA && dA && dB && workspace, QLORA_EINVAL,
+               "NULL pointer argument");
+    QL_REQUIRE(aligned(Xq, 16) && aligned(dY, 16) && aligned(Wq, 16) && (!dX || aligned(dX, 16)) &&
+                   aligned(workspace, 256),
+               QLORA_EALIGN, "Xq, dY, dX, Wq must be 16-byte aligned, workspace 256-byte aligned");
+    QL_REQUIRE(aligned(sx, 4) && aligned(sw, 4) && aligned(A, 4) && aligned(B, 4) && aligned(xA, 4) &&
+                   aligned(dA, 4) && aligned(dB, 4) && (!dbias || aligned(dbias, 4)),
+               QLORA_EALIGN, "fp32 vectors must be 4-byte aligned");
+    QL_REQUIRE(M <= kRankQMaxRows, QLORA_EUNSUPPORTED, "more than 1047552 rows would overflow the int32 sums");
+    DxEpilogue checked;
+    rc = dx_epilogue(epilogue, checked);
+    if (rc != QLORA_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        rc = cuda_status(cudaMemsetAsync(dA, 0, sizeof(float) * d->K * d->r, s), "memset dA");
+        if (rc == QLORA_OK)
+            rc = cuda_status(cudaMemsetAsync(dB, 0, sizeof(float) * d->r * d->N, s), "memset dB");
+        if (rc == QLORA_OK && dbias)
+            rc = cuda_status(cudaMemsetAsync(dbias, 0, sizeof(float) * d->N, s), "memset dbias");
+        return rc;
+    }
+    QL_REQUIRE(workspace_bytes >= qlora_ckpt_workspace_bytes(d, M), QLORA_EINVAL, "workspace too small");
+    rc = lora_grad_dy_impl(d, M, dY, B, xA, dB, dbias, nullptr, workspace, workspace_bytes, stream, true);
+    if (rc != QLORA_OK) return rc;
+    SideStream* ss = (dX && M >= kSideStreamMinM) ? side_stream() : nullptr;
+    if (ss) {
+        // as qlora_backward: the X pass beside the dX GEMM
+        rc = cuda_status(cudaEventRecord(ss->fork, s), "backward fork");
+        if (rc != QLORA_OK) return rc;
+        rc = gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, epilogue);
+        const int rc_wait = cuda_status(cudaStreamWaitEvent(ss->st, ss->fork, 0), "backward fork");
+        const int rc_x = rc_wait == QLORA_OK ? grad_x_ckpt(d, M, Xq, sx, dA, workspace, ss->st) : rc_wait;
+        const int rc_join = cuda_status(cudaEventRecord(ss->join, ss->st), "backward join");
+        const int rc_join2 = rc_join == QLORA_OK
+                                 ? cuda_status(cudaStreamWaitEvent(s, ss->join, 0), "backward join")
+                                 : rc_join;
+        if (rc != QLORA_OK) return rc;
+        if (rc_x != QLORA_OK) return rc_x;
+        return rc_join2;
+    }
+    if (dX) {
+        rc = gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, epilogue);
+        if (rc != QLORA_OK) return rc;
+    }
+    return grad_x_ckpt(d, M, Xq, sx, dA, workspace, s);
+}
+
+static int check_ckpt(const void* T, int rows, int cols, qlora_dtype dtype, const void* q, const void* scales) {
+    QL_REQUIRE(rows >= 0 && cols >= 1, QLORA_ESHAPE, "rows must be >= 0 and cols >= 1");
+    QL_REQUIRE(T && q && scales, QLORA_EINVAL, "NULL pointer argument");
+    QL_REQUIRE(dtype == QLORA_F32 || dtype == QLORA_BF16, QLORA_EINVAL, "unknown activation dtype");
+    QL_REQUIRE(aligned(T, 16) && aligned(q, 16) && aligned(scales, 4), QLORA_EALIGN,
+               "T and q must be 16-byte aligned, scales 4-byte aligned");
+    return QLORA_OK;
+}
+
+int qlora_ckpt_save(const void* T, int rows, int cols, qlora_dtype dtype, int8_t* q, float* scales, void* stream) {
+    int rc = check_ckpt(T, rows, cols, dtype, q, scales);
+    if (rc != QLORA_OK || rows == 0) return rc;
+    return cuda_status(launch_ckpt_save(dtype == QLORA_BF16 ? kBF16 : kF32, T, rows, cols, q, scales,
+                                        static_cast<cudaStream_t>(stream)),
+                       "checkpoint save launch");
+}
+
+int qlora_ckpt_load(const int8_t* q, const float* scales, int rows, int cols, int block, qlora_dtype dtype, void* T,
+                    void* stream) {
+    int rc = check_ckpt(T, rows, cols, dtype, q, scales);
+    if (rc != QLORA_OK) return rc;
+    QL_REQUIRE(block == 0 || block == kCkptBlock, QLORA_EUNSUPPORTED,
+               "block must be 32 columns, or 0 for one scale per row");
+    if (rows == 0) return QLORA_OK;
+    return cuda_status(launch_ckpt_load(dtype == QLORA_BF16 ? kBF16 : kF32, q, scales, rows, cols, block, T,
+                                        static_cast<cudaStream_t>(stream)),
+                       "checkpoint load launch");
 }
 
 int qlora_merge(const qlora_layer_desc* d, const int8_t* Wq, const float* sw, const float* A,

@@ -28,6 +28,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "dx_common.cuh"
+#include "act_epilogue.cuh"
 
 namespace qlora {
 
@@ -91,7 +92,9 @@ __device__ __forceinline__ void send_partials(uint32_t tmem, int q, int lane, in
 // packed tile ([128 rows][64 bytes], no swizzle) and the epilogue warps,
 // idle until the accumulator is final, expand it into the int8 tile in the
 // layout the TMA would have written (16-byte chunk c of row n at c ^ (n % 8)).
-template <typename OutT, int RMAX, bool W4>
+// EX: Y = act(Z) + res with Z kept in 8 bits (act_epilogue.cuh): a warp's 32
+// channels of a token are one block of the checkpoint.
+template <typename OutT, int RMAX, bool W4, bool EX>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     k2_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     SmallArgs a, FwdEpilogue ep, int* status) {
@@ -246,17 +249,39 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float bn = (nok && ep.bias) ? __ldg(ep.bias + n) : 0.f;
         OutT* Y = static_cast<OutT*>(ep.Y);
         const float* tab = reinterpret_cast<const float*>(smem + kRing);
+        // EX: the residual of the next token is loaded a token ahead (it may
+        // lie in Y's own buffer: read here before it is written)
+        const OutT* res = EX ? static_cast<const OutT*>(ep.res) : nullptr;
+        auto res_at = [&](int cl) {
+            const int m = static_cast<int>(rank) * W + cl;
+            return EX && res && nok && cl < W && m < a.M ? ActIO<OutT>::to_f(res[static_cast<size_t>(m) * a.N + n]) : 0.f;
+        };
+        float rnext = res_at(0);
         for (int cl = 0; cl < W; ++cl) {
             const int m = static_cast<int>(rank) * W + cl;
             if (m >= a.M) break;
             int acc = 0;
             for (int qq = 0; qq < a.S; ++qq) acc += static_cast<int>(recv[(qq * W + cl) * kCh + row]);
-            if (!nok) continue;
+            if (!EX && !nok) continue;
             const float* tr = tab + cl * (RMAX + 1);
             float lora = 0.f;
 #pragma unroll
             for (int j = 0; j < RMAX; ++j) lora = fmaf(tr[j], bj[j], lora);
             float y = fmaf(static_cast<float>(acc), __fmul_rn(tr[RMAX], swn), fmaf(ep.c, lora, bn));
+            if constexpr (EX) {
+                const float rv = rnext;
+                rnext = res_at(cl + 1);
+                if (ep.zq) {  // lanes past N hold z = 0
+                    float inv, scale;
+                    ckpt_scale(__reduce_max_sync(0xffffffffu, abs_bits(nok ? y : 0.f)), inv, scale);
+                    if (nok) ep.zq[static_cast<size_t>(m) * a.N + n] = static_cast<int8_t>(quant_code(y, inv));
+                    if (lane == 0 && nok) ep.zs[static_cast<size_t>(n / kCkptBlock) * a.M + m] = scale;
+                }
+                float z[1] = {y};
+                act_apply(ep.act, z);
+                if (nok) Y[static_cast<size_t>(m) * a.N + n] = ActIO<OutT>::from_f(res ? z[0] + rv : z[0]);
+                continue;
+            }
             if (ep.relu) y = fmaxf(y, 0.f);
             Y[static_cast<size_t>(m) * a.N + n] = ActIO<OutT>::from_f(y);
             if (ep.acc) ep.acc[static_cast<size_t>(m) * a.N + n] = acc;
@@ -280,7 +305,8 @@ constexpr uint32_t kDqTileBytes = kCh * 64 * 2;
 constexpr uint32_t kCodeBytes = 64 * kCh;
 
 // W4: packed int4 codes Wp [N, K/2]; a stage's codes are [64 rows][64 bytes].
-template <int RMAX, bool W4>
+// EX: dX = (.) * act'(z) + add (act_epilogue.cuh).
+template <int RMAX, bool W4, bool EX>
 __global__ void __launch_bounds__(kDxThreads, 1)
     k3_small_kernel(const __grid_constant__ CUtensorMap tmDY, const __grid_constant__ CUtensorMap tmW,
                     const float* __restrict__ sw, SmallArgs a, DxEpilogue ep, int* status) {
@@ -475,6 +501,18 @@ __global__ void __launch_bounds__(kDxThreads, 1)
         __nv_bfloat16* dX = static_cast<__nv_bfloat16*>(ep.dX);
         const __nv_bfloat16* gate = static_cast<const __nv_bfloat16*>(ep.gate);
         const float* tab = reinterpret_cast<const float*>(smem + kRing);
+        // EX: z and the added gradient of the next token, loaded a token ahead
+        const __nv_bfloat16* add = EX ? static_cast<const __nv_bfloat16*>(ep.add) : nullptr;
+        float znext = 0.f, anext = 0.f;
+        auto fetch = [&](int cl) {
+            const int m = static_cast<int>(rank) * W + cl;
+            if (!EX || !kok || cl >= W || m >= a.M) return;
+            if (ep.act != kActNone)
+                znext = static_cast<float>(ep.zq[static_cast<size_t>(m) * a.K + k]) *
+                        ep.zs[static_cast<size_t>(k / kCkptBlock) * a.M + m];
+            if (add) anext = __bfloat162float(add[static_cast<size_t>(m) * a.K + k]);
+        };
+        fetch(0);
         for (int cl = 0; cl < W; ++cl) {
             const int m = static_cast<int>(rank) * W + cl;
             if (m >= a.M) break;
@@ -486,6 +524,14 @@ __global__ void __launch_bounds__(kDxThreads, 1)
 #pragma unroll
             for (int j = 0; j < RMAX; ++j) l = fmaf(tr[j], aj[j], l);
             float y = acc + l;
+            if constexpr (EX) {
+                const float zv[1] = {znext};
+                const float av = anext;
+                fetch(cl + 1);
+                float yv[1] = {y};
+                slope_apply(ep.act, zv, yv);
+                y = add ? yv[0] + av : yv[0];
+            }
             if (gate && !(__bfloat162float(gate[static_cast<size_t>(m) * a.K + k]) > 0.f)) y = 0.f;
             dX[static_cast<size_t>(m) * a.K + k] = __float2bfloat16_rn(y);
         }
@@ -548,15 +594,19 @@ cudaError_t launch_gemm_i8_fwd_small(Act act, const int8_t* Xq, const int8_t* Wq
         if (e != cudaSuccess) return e;
         return launch_k(kern, grid, dim3(kFwdThreads), smem, s, a.S, tw, tx, a, ep, status);
     };
-    auto by_w4 = [&](auto k8, auto k4) { return w4 ? run(k4) : run(k8); };
+    // by rank, then by codes and epilogue form
+#define QL_FWD_SMALL(T, R)                                                                          \
+    (ep.ex ? (w4 ? run(k2_small_kernel<T, R, true, true>) : run(k2_small_kernel<T, R, false, true>)) \
+           : (w4 ? run(k2_small_kernel<T, R, true, false>) : run(k2_small_kernel<T, R, false, false>)))
     if (act == kBF16) {
-        if (ep.r <= 4) return by_w4(k2_small_kernel<__nv_bfloat16, 4, false>, k2_small_kernel<__nv_bfloat16, 4, true>);
-        if (ep.r <= 8) return by_w4(k2_small_kernel<__nv_bfloat16, 8, false>, k2_small_kernel<__nv_bfloat16, 8, true>);
-        return by_w4(k2_small_kernel<__nv_bfloat16, 16, false>, k2_small_kernel<__nv_bfloat16, 16, true>);
+        if (ep.r <= 4) return QL_FWD_SMALL(__nv_bfloat16, 4);
+        if (ep.r <= 8) return QL_FWD_SMALL(__nv_bfloat16, 8);
+        return QL_FWD_SMALL(__nv_bfloat16, 16);
     }
-    if (ep.r <= 4) return by_w4(k2_small_kernel<float, 4, false>, k2_small_kernel<float, 4, true>);
-    if (ep.r <= 8) return by_w4(k2_small_kernel<float, 8, false>, k2_small_kernel<float, 8, true>);
-    return by_w4(k2_small_kernel<float, 16, false>, k2_small_kernel<float, 16, true>);
+    if (ep.r <= 4) return QL_FWD_SMALL(float, 4);
+    if (ep.r <= 8) return QL_FWD_SMALL(float, 8);
+    return QL_FWD_SMALL(float, 16);
+#undef QL_FWD_SMALL
 }
 
 cudaError_t launch_gemm_dx_small(const void* dY, const int8_t* Wq, const float* sw, int M, int N, int K,
@@ -587,9 +637,13 @@ cudaError_t launch_gemm_dx_small(const void* dY, const int8_t* Wq, const float* 
         if (e != cudaSuccess) return e;
         return launch_k(kern, grid, dim3(kDxThreads), smem, s, a.S, ty, tw, sw, a, ep, status);
     };
-    if (ep.r <= 4) return w4 ? run(k3_small_kernel<4, true>) : run(k3_small_kernel<4, false>);
-    if (ep.r <= 8) return w4 ? run(k3_small_kernel<8, true>) : run(k3_small_kernel<8, false>);
-    return w4 ? run(k3_small_kernel<16, true>) : run(k3_small_kernel<16, false>);
+#define QL_DX_SMALL(R)                                                                    \
+    (ep.ex ? (w4 ? run(k3_small_kernel<R, true, true>) : run(k3_small_kernel<R, false, true>)) \
+           : (w4 ? run(k3_small_kernel<R, true, false>) : run(k3_small_kernel<R, false, false>)))
+    if (ep.r <= 4) return QL_DX_SMALL(4);
+    if (ep.r <= 8) return QL_DX_SMALL(8);
+    return QL_DX_SMALL(16);
+#undef QL_DX_SMALL
 }
 
 }  // namespace qlora

@@ -37,7 +37,15 @@ EXPORTED = ("qlora_quantize_weight", "qlora_workspace_bytes", "qlora_forward",
             "qlora_outlier_cap", "qlora_outlier_workspace_bytes", "qlora_outlier_quantize",
             "qlora_outlier_forward", "qlora_outlier_backward", "qlora_permute",
             "qlora_fp8_quantize", "qlora_fp8_gemm", "qlora_fp8_colsum_workspace_bytes",
-            "qlora_fp8_quantize_colsum", "qlora_fp8_gemm_workspace_bytes", "qlora_fp8_gemm_ws")
+            "qlora_fp8_quantize_colsum", "qlora_fp8_gemm_workspace_bytes", "qlora_fp8_gemm_ws",
+            "qlora_gemm_forward_act", "qlora_gemm_forward_act_int4", "qlora_forward_act",
+            "qlora_gemm_dx_act", "qlora_gemm_dx_act_int4", "qlora_ckpt_scales",
+            "qlora_ckpt_workspace_bytes", "qlora_lora_grad_x_ckpt", "qlora_backward_ckpt",
+            "qlora_ckpt_save", "qlora_ckpt_load")
+
+# qlora_activation
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+CKPT_BLOCK = 32  # columns of a row that share a scale in an 8-bit checkpoint
 
 
 class QLoraError(RuntimeError):
@@ -61,6 +69,18 @@ class OutlierKernelStruct(ctypes.Structure):
                 ("par", ctypes.c_void_p), ("start_nk", ctypes.c_void_p),
                 ("ent_nk", ctypes.c_void_p), ("start_kn", ctypes.c_void_p),
                 ("ent_kn", ctypes.c_void_p), ("cap", ctypes.c_int)]
+
+
+class FwdEpilogue(ctypes.Structure):
+    """qlora_fwd_epilogue: activation, residual and 8-bit checkpoint of Z."""
+    _fields_ = [("act", ctypes.c_int), ("residual", ctypes.c_void_p), ("zq", ctypes.c_void_p),
+                ("zs", ctypes.c_void_p)]
+
+
+class DxEpilogue(ctypes.Structure):
+    """qlora_dx_epilogue: activation, its z in 8 bits and an added gradient."""
+    _fields_ = [("act", ctypes.c_int), ("zq", ctypes.c_void_p), ("zs", ctypes.c_void_p),
+                ("add", ctypes.c_void_p)]
 
 
 def _load():
@@ -140,6 +160,24 @@ def _load():
     lib.qlora_fp8_gemm.restype = I
     lib.qlora_permute.argtypes = [P, P, I, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int), I, P]
     lib.qlora_permute.restype = I
+    FE, DE = ctypes.POINTER(FwdEpilogue), ctypes.POINTER(DxEpilogue)
+    lib.qlora_gemm_forward_act.argtypes = [D, I, P, P, P, P, P, P, P, FE, P, P]
+    lib.qlora_gemm_forward_act_int4.argtypes = [D, I, P, P, P, P, P, P, P, FE, P, P]
+    lib.qlora_forward_act.argtypes = [D, I, P, P, P, P, P, P, FE, P, P, P, P, P]
+    lib.qlora_gemm_dx_act.argtypes = [D, I, P, P, P, P, DE, P, P, Z, P]
+    lib.qlora_gemm_dx_act_int4.argtypes = [D, I, P, P, P, P, DE, P, P, Z, P]
+    lib.qlora_ckpt_scales.argtypes = [I, I]
+    lib.qlora_ckpt_scales.restype = Z
+    lib.qlora_ckpt_workspace_bytes.argtypes = [D, I]
+    lib.qlora_ckpt_workspace_bytes.restype = Z
+    lib.qlora_lora_grad_x_ckpt.argtypes = [D, I, P, P, P, P, Z, P]
+    lib.qlora_backward_ckpt.argtypes = [D, I, P, P, P, P, P, P, P, P, DE, P, P, P, P, P, Z, P]
+    lib.qlora_ckpt_save.argtypes = [P, I, I, I, P, P, P]
+    lib.qlora_ckpt_load.argtypes = [P, P, I, I, I, I, P, P]
+    for f in (lib.qlora_gemm_forward_act, lib.qlora_gemm_forward_act_int4, lib.qlora_forward_act,
+              lib.qlora_gemm_dx_act, lib.qlora_gemm_dx_act_int4, lib.qlora_lora_grad_x_ckpt,
+              lib.qlora_backward_ckpt, lib.qlora_ckpt_save, lib.qlora_ckpt_load):
+        f.restype = I
     lib.qlora_set_rank_pass_rows.argtypes = [I]
     lib.qlora_set_rank_pass_rows.restype = I
     lib.qlora_selftest_wait_timeout.argtypes = [ctypes.c_uint, P]
@@ -597,3 +635,223 @@ def merge(layer: Layer, stream=None):
     sw2 = torch.empty_like(layer.sw)
     qlora_merge(layer.desc(), layer.Wq, layer.sw, layer.A, layer.B, Wq2, sw2, stream)
     return Wq2, sw2
+
+
+# --------------------------------------------------------------------------
+# activation and residual in the epilogues, 8-bit activation checkpoints
+# --------------------------------------------------------------------------
+def act_fn(name: str) -> int:
+    """qlora_activation of "none", "relu", "gelu", "gelu_tanh" or "silu"."""
+    if name not in ACTIVATIONS:
+        raise ValueError("act must be one of %s" % ", ".join(ACTIVATIONS))
+    return ACTIVATIONS[name]
+
+
+@dataclass
+class Checkpoint:
+    """What a layer's forward keeps for its backward: the input as row codes
+    (Xq, sx), xA = X . A and, where it was asked for, the pre-activation Z in 8
+    bits (zq [M, N], zs [ceil(N / 32), M])."""
+
+    Xq: torch.Tensor
+    sx: torch.Tensor
+    xA: torch.Tensor
+    zq: Optional[torch.Tensor] = None
+    zs: Optional[torch.Tensor] = None
+
+    @property
+    def z(self):
+        """(zq, zs), as the backward of the layer above takes it."""
+        return None if self.zq is None else (self.zq, self.zs)
+
+
+def _expect(t, name: str, shape, dtype, device):
+    """Checks one tensor argument; returns its address (None for None)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError("%s must be %s of shape %s" % (name, dtype, tuple(shape)))
+    if t.device != device:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _on_device(t: torch.Tensor, what: str, stream):
+    """The stream's handle; the library works on the current device, so the
+    tensors have to be there."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (what, t.device, torch.cuda.current_device()))
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def ckpt_buffers(M: int, N: int, device=None):
+    """Empty buffers (q [M, N] int8, scales [ceil(N / 32), M] fp32) of an 8-bit checkpoint."""
+    dev = device or "cuda"
+    return (torch.empty((M, N), dtype=torch.int8, device=dev),
+            torch.empty((-(-N // CKPT_BLOCK), M), dtype=torch.float32, device=dev))
+
+
+def ckpt_workspace(d: LayerDesc, M: int, device=None) -> torch.Tensor:
+    """A uint8 device buffer big enough for backward_ckpt at M tokens."""
+    n = int(_lib.qlora_ckpt_workspace_bytes(ctypes.byref(d), int(M)))
+    if n == 0:
+        raise QLoraError(-1, "invalid layer descriptor or more than 1047552 tokens")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _check_layer_tensors(layer: "Layer", dev):
+    K, N, r = layer.K, layer.N, layer.r
+    f32 = torch.float32
+    return (_expect(layer.Wq, "Wq", (N, K), torch.int8, dev), _expect(layer.sw, "sw", (N,), f32, dev),
+            _expect(layer.bias, "bias", (N,), f32, dev), _expect(layer.A, "A", (K, r), f32, dev),
+            _expect(layer.B, "B", (r, N), f32, dev))
+
+
+def forward_act(layer: Layer, X: torch.Tensor, act: str = "none", residual: Optional[torch.Tensor] = None,
+                save_z: bool = False, keep: Optional[Checkpoint] = None, Y: Optional[torch.Tensor] = None,
+                stream=None):
+    """Y = act(Z) + residual with Z the layer's output; returns (Y, Checkpoint).
+
+    The checkpoint holds the input's codes (and, with ``save_z``, Z in 8
+    bits); ``keep`` gives its buffers, else they are allocated.  ``residual``
+    may be ``Y`` itself.  Gradients: ``backward_ckpt``."""
+    fn = act_fn(act)
+    s = _on_device(X, "X", stream)
+    dev, M, K, N, r = X.device, X.shape[0], layer.K, layer.N, layer.r
+    x = _expect(X, "X", (M, K), layer.act, dev)
+    wq, sw, bias, a, b = _check_layer_tensors(layer, dev)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=layer.act, device=dev)
+    if keep is None:
+        zq, zs = ckpt_buffers(M, N, dev) if save_z else (None, None)
+        keep = Checkpoint(torch.empty((M, K), dtype=torch.int8, device=dev),
+                          torch.empty((M,), dtype=torch.float32, device=dev),
+                          torch.empty((M, r), dtype=torch.float32, device=dev), zq, zs)
+    if save_z and keep.zq is None:
+        raise ValueError("save_z needs zq and zs in keep")
+    f32 = torch.float32
+    y, xq = _expect(Y, "Y", (M, N), layer.act, dev), _expect(keep.Xq, "Xq", (M, K), torch.int8, dev)
+    sx, xa = _expect(keep.sx, "sx", (M,), f32, dev), _expect(keep.xA, "xA", (M, r), f32, dev)
+    ep = FwdEpilogue(fn, _expect(residual, "residual", (M, N), layer.act, dev), None, None)
+    if save_z:
+        ep.zq = _expect(keep.zq, "zq", (M, N), torch.int8, dev)
+        ep.zs = _expect(keep.zs, "zs", (-(-N // CKPT_BLOCK), M), f32, dev)
+    if M > 0:
+        _check(_lib.qlora_forward_act(layer.desc(), M, x, wq, sw, bias, a, b, ep, y, xq, sx, xa, s))
+    return Y, keep
+
+
+def _dx_epilogue(act: str, z, add, M: int, K: int, dtype, dev) -> DxEpilogue:
+    fn = act_fn(act)
+    if fn and z is None:
+        raise ValueError("the gradient of %s needs z, the 8-bit checkpoint of its input" % act)
+    ep = DxEpilogue(fn, None, None, _expect(add, "add", (M, K), dtype, dev))
+    if fn:
+        ep.zq = _expect(z[0], "zq", (M, K), torch.int8, dev)
+        ep.zs = _expect(z[1], "zs", (-(-K // CKPT_BLOCK), M), torch.float32, dev)
+    return ep
+
+
+def backward_ckpt(layer: Layer, keep: Checkpoint, dY: torch.Tensor, ws: torch.Tensor, act: str = "none", z=None,
+                  add: Optional[torch.Tensor] = None, dX: Optional[torch.Tensor] = None, want_dx: bool = True,
+                  want_dbias: bool = True, stream=None):
+    """The layer's gradients from the checkpoint its forward kept: returns
+    (dX or None, dA, dB, dbias or None).
+
+    ``act`` and ``z`` (the ``Checkpoint.z`` of the layer below) name the
+    activation that produced this layer's input: dX is taken back through it.
+    ``add`` is added to dX (the gradient of a skip connection; it may be ``dX``
+    itself).  ``ws``: ``ckpt_workspace``."""
+    s = _on_device(dY, "dY", stream)
+    dev, M, K, N, r = dY.device, dY.shape[0], layer.K, layer.N, layer.r
+    f32 = torch.float32
+    dy = _expect(dY, "dY", (M, N), layer.act, dev)
+    wq, sw, _, a, b = _check_layer_tensors(layer, dev)
+    xq, sx = _expect(keep.Xq, "Xq", (M, K), torch.int8, dev), _expect(keep.sx, "sx", (M,), f32, dev)
+    xa = _expect(keep.xA, "xA", (M, r), f32, dev)
+    ep = _dx_epilogue(act, z, add, M, K, layer.act, dev)
+    if not want_dx:
+        dX = None
+    elif dX is None:
+        dX = torch.empty((M, K), dtype=layer.act, device=dev)
+    w = _expect(ws, "ws", ws.shape, torch.uint8, dev)
+    dA = torch.empty((K, r), dtype=f32, device=dev)
+    dB = torch.empty((r, N), dtype=f32, device=dev)
+    dbias = torch.empty((N,), dtype=f32, device=dev) if want_dbias else None
+    if M == 0:
+        for g in (dA, dB, dbias):
+            if g is not None:
+                g.zero_()
+        return dX, dA, dB, dbias
+    _check(_lib.qlora_backward_ckpt(layer.desc(), M, xq, sx, dy, wq, sw, a, b, xa, ep,
+                                    _expect(dX, "dX", (M, K), layer.act, dev), dA.data_ptr(), dB.data_ptr(),
+                                    dbias.data_ptr() if want_dbias else None, w, ws.numel(), s))
+    return dX, dA, dB, dbias
+
+
+def qlora_gemm_forward_act(d: LayerDesc, M: int, Xq, sx, Wq, sw, bias, xA, B, Y, act: str = "none", residual=None,
+                           z=None, stream=None):
+    """qlora_gemm_forward, then act and residual in its epilogue; z = (zq, zs)
+    receives the 8-bit checkpoint of the pre-activation.  A uint8 Wq [N, K/2]
+    is a packed int4 kernel."""
+    ep = FwdEpilogue(act_fn(act), None if residual is None else residual.data_ptr(),
+                     None if z is None else z[0].data_ptr(), None if z is None else z[1].data_ptr())
+    for t in (residual,) + (tuple(z) if z is not None else ()):
+        _ptr(t)
+    f = _lib.qlora_gemm_forward_act_int4 if Wq.dtype == torch.uint8 else _lib.qlora_gemm_forward_act
+    _check(f(ctypes.byref(d), int(M), _ptr(Xq), _ptr(sx), _ptr(Wq), _ptr(sw), _ptr(bias), _ptr(xA), _ptr(B),
+             ctypes.byref(ep), _ptr(Y), _stream(stream)))
+
+
+def qlora_gemm_dx_act(d: LayerDesc, M: int, dY, Wq, sw, A, dX, ws, act: str = "none", z=None, add=None, stream=None):
+    """qlora_gemm_dx, then times act'(z) and plus `add` in its epilogue.  A
+    uint8 Wq [N, K/2] is a packed int4 kernel."""
+    ep = DxEpilogue(act_fn(act), None if z is None else z[0].data_ptr(), None if z is None else z[1].data_ptr(),
+                    None if add is None else add.data_ptr())
+    for t in (add,) + (tuple(z) if z is not None else ()):
+        _ptr(t)
+    f = _lib.qlora_gemm_dx_act_int4 if Wq.dtype == torch.uint8 else _lib.qlora_gemm_dx_act
+    _check(f(ctypes.byref(d), int(M), _ptr(dY), _ptr(Wq), _ptr(sw), _ptr(A), ctypes.byref(ep), _ptr(dX), _ptr(ws),
+             ws.numel(), _stream(stream)))
+
+
+def qlora_lora_grad_x_ckpt(d: LayerDesc, M: int, Xq, sx, dA, ws, stream=None):
+    """dA from the input's kept codes; ws: ckpt_workspace, its G from the dY pass."""
+    _check(_lib.qlora_lora_grad_x_ckpt(ctypes.byref(d), int(M), _ptr(Xq), _ptr(sx), _ptr(dA), _ptr(ws), ws.numel(),
+                                       _stream(stream)))
+
+
+def ckpt_save(T: torch.Tensor, out=None, stream=None):
+    """The 8-bit checkpoint (q [M, N], scales [ceil(N / 32), M]) of T [M, N]."""
+    s = _on_device(T, "T", stream)
+    if T.dim() != 2:
+        raise ValueError("T must have two axes")
+    M, N = T.shape
+    q, scales = out if out is not None else ckpt_buffers(M, N, T.device)
+    _check(_lib.qlora_ckpt_save(_expect(T, "T", (M, N), T.dtype, T.device), M, N, act_code(T.dtype),
+                                _expect(q, "q", (M, N), torch.int8, T.device),
+                                _expect(scales, "scales", (-(-N // CKPT_BLOCK), M), torch.float32, T.device),
+                                s) if M > 0 else 0)
+    return q, scales
+
+
+def ckpt_load(q: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values of codes q [M, N]: with scales [ceil(N / 32), M] of an 8-bit
+    checkpoint, or [M] of row codes (Xq, sx)."""
+    s = _on_device(q, "q", stream)
+    if q.dim() != 2:
+        raise ValueError("q must have two axes")
+    M, N = q.shape
+    block = 0 if scales.dim() == 1 else CKPT_BLOCK
+    T = out if out is not None else torch.empty((M, N), dtype=dtype, device=q.device)
+    shape = (M,) if block == 0 else (-(-N // CKPT_BLOCK), M)
+    _check(_lib.qlora_ckpt_load(_expect(q, "q", (M, N), torch.int8, q.device),
+                                _expect(scales, "scales", shape, torch.float32, q.device), M, N, block,
+                                act_code(T.dtype), _expect(T, "out", (M, N), T.dtype, q.device),
+                                s) if M > 0 else 0)
+    return T
