@@ -160,17 +160,13 @@ __device__ __forceinline__ void ckpt_scale(uint32_t top, float& inv, float& scal
     }
 }
 
-// Stores the codes of one block (columns n .. n + 31 of row `row`) and its
-// scale.  Columns >= N hold zeros and are not written.
-__device__ __forceinline__ void ckpt_store(const float (&z)[kCkptBlock], int8_t* __restrict__ zq,
-                                           float* __restrict__ zs, int row, int M, int n, int N) {
+// Codes and scale of one block.
+__device__ __forceinline__ float ckpt_codes(const float (&z)[kCkptBlock], uint32_t (&w)[kCkptBlock / 4]) {
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < kCkptBlock; ++e) top = max(top, abs_bits(z[e]));
     float inv, scale;
     ckpt_scale(top, inv, scale);
-    zs[static_cast<size_t>(n / kCkptBlock) * M + row] = scale;
-    uint32_t w[kCkptBlock / 4];
 #pragma unroll
     for (int i = 0; i < kCkptBlock / 8; ++i) {
         float f[8];
@@ -180,6 +176,15 @@ __device__ __forceinline__ void ckpt_store(const float (&z)[kCkptBlock], int8_t*
         w[2 * i] = c.x;
         w[2 * i + 1] = c.y;
     }
+    return scale;
+}
+
+// Stores the codes of one block (columns n .. n + 31 of row `row`) and its
+// scale.  Columns >= N hold zeros and are not written.
+__device__ __forceinline__ void ckpt_store(const float (&z)[kCkptBlock], int8_t* __restrict__ zq,
+                                           float* __restrict__ zs, int row, int M, int n, int N) {
+    uint32_t w[kCkptBlock / 4];
+    zs[static_cast<size_t>(n / kCkptBlock) * M + row] = ckpt_codes(z, w);
     int8_t* dst = zq + static_cast<size_t>(row) * N + n;
     if (N % 16 == 0) {  // whole 16-byte chunks lie inside the row or outside it
 #pragma unroll

@@ -53,6 +53,11 @@ bool gemm_fwd_pair_applies(Act act, int M, int N, int K, int r);
 cudaError_t launch_gemm_i8_fwd_pair(const int8_t* Xq, const int8_t* Wq, int M, int N, int K,
                                     const FwdEpilogue& ep, int* status, cudaStream_t s, bool w4);
 
+// With activation, residual and checkpoint, rows by TMA (k2_pair_act.cu).
+bool gemm_fwd_pair_act_applies(Act act, int M, int N, int K, int r);
+cudaError_t launch_gemm_i8_fwd_pair_act(const int8_t* Xq, const int8_t* Wq, int M, int N, int K,
+                                        const FwdEpilogue& ep, int* status, cudaStream_t s);
+
 // ---------------------------------------------------------------- K3
 // Outlier-compensated int8 kernel as a GEMM operand (outlier.cu): uint8
 // affine codes [rows, cols] with rows the contraction, one scale and bias per
@@ -128,6 +133,14 @@ cudaError_t launch_gemm_i8_fwd_small(Act act, const int8_t* Xq, const int8_t* Wq
                                      const FwdEpilogue& ep, int* status, cudaStream_t s, bool w4);
 cudaError_t launch_gemm_dx_small(const void* dY, const int8_t* Wq, const float* sw, int M, int N, int K,
                                  const DxEpilogue& ep, int* status, cudaStream_t s, bool w4);
+
+// dX of large bf16 layers from a de-quantized copy of the kernel
+// (k3_pair_act.cu): bytes of that copy where it is used, else 0; Wd [N,K] =
+// bf16(Wq sw) from int8 or packed int4 codes; dX with the EX epilogue.
+size_t dx_dense_bytes(Act act, int M, int N, int K, int r);
+cudaError_t launch_dequantize(const void* Wq, const float* sw, int N, int K, bool w4, void* Wd, cudaStream_t s);
+cudaError_t launch_gemm_dx_dense(const void* dY, const void* Wd, int M, int N, int K, const DxEpilogue& ep,
+                                 int* status, cudaStream_t s);
 
 // Axis permutation of a row-major tensor of up to kMaxPermAxes axes
 // (permute.cu): dst axis d is src axis perm[d].

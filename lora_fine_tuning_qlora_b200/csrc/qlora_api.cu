@@ -514,6 +514,11 @@ int qlora_lora_grad_b(const qlora_layer_desc* d, int M, const void* dY, const fl
                        "dB pass launch");
 }
 
+// Where a workspace of qlora_ckpt_workspace_bytes holds the de-quantized kernel.
+static size_t ckpt_dense_offset(const qlora_layer_desc* d, int M) {
+    return layout_for(*d, M).total + align256(rank_q_digit_bytes(M, d->r));
+}
+
 // The checks of a dX epilogue and its part of the launch arguments.
 static int dx_epilogue(const qlora_dx_epilogue* x, DxEpilogue& ep) {
     if (!x) return QLORA_OK;
@@ -558,6 +563,17 @@ static int gemm_dx_impl(const qlora_layer_desc* d, int M, const void* dY, const 
     ep.c = lora_scale(d);
     ep.dX = dX;
     ep.gate = gate;
+    // many rows and a workspace with room for it: the kernel de-quantized once
+    const size_t dense = x ? dx_dense_bytes(act_of(d), M, d->N, d->K, d->r) : 0;
+    const size_t dense_at = ckpt_dense_offset(d, M);
+    if (dense && workspace_bytes >= dense_at + dense) {
+        uint8_t* Wd = const_cast<uint8_t*>(static_cast<const uint8_t*>(workspace)) + dense_at;
+        rc = cuda_status(launch_dequantize(Wq, sw, d->N, d->K, w4, Wd, static_cast<cudaStream_t>(stream)),
+                         "de-quantize launch");
+        if (rc != QLORA_OK) return rc;
+        return cuda_status(launch_gemm_dx_dense(dY, Wd, M, d->N, d->K, ep, status, static_cast<cudaStream_t>(stream)),
+                           "dX GEMM launch");
+    }
     return cuda_status(launch_gemm_dx(act_of(d), dY, Wq, sw, M, d->N, d->K, ep, status,
                                       static_cast<cudaStream_t>(stream), w4),
                        "dX GEMM launch");
@@ -744,7 +760,8 @@ size_t qlora_ckpt_scales(int rows, int cols) {
 size_t qlora_ckpt_workspace_bytes(const qlora_layer_desc* d, int M) {
     if (check_desc(d) != QLORA_OK || M < 0 || M > kRankQMaxRows) return 0;
     if (M == 0) return 256;
-    return layout_for(*d, M).total + align256(rank_q_digit_bytes(M, d->r));
+    const Act act = d->act_dtype == QLORA_BF16 ? kBF16 : kF32;
+    return ckpt_dense_offset(d, M) + align256(dx_dense_bytes(act, M, d->N, d->K, d->r));
 }
 
 // Shared by the step-level call and the composite, both of which have
@@ -772,7 +789,7 @@ int qlora_lora_grad_x_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, c
     QL_REQUIRE(M <= kRankQMaxRows, QLORA_EUNSUPPORTED, "more than 1047552 rows would overflow the int32 sums");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (M == 0) return cuda_status(cudaMemsetAsync(dA, 0, sizeof(float) * d->K * d->r, s), "memset dA");
-    QL_REQUIRE(workspace_bytes >= qlora_ckpt_workspace_bytes(d, M), QLORA_EINVAL, "workspace too small");
+    QL_REQUIRE(workspace_bytes >= ckpt_dense_offset(d, M), QLORA_EINVAL, "workspace too small");
     return grad_x_ckpt(d, M, Xq, sx, dA, workspace, s);
 }
 
@@ -794,6 +811,7 @@ int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, cons
     DxEpilogue checked;
     rc = dx_epilogue(epilogue, checked);
     if (rc != QLORA_OK) return rc;
+    const qlora_dx_epilogue none_or = epilogue ? *epilogue : qlora_dx_epilogue{QLORA_ACT_NONE, nullptr, nullptr, nullptr};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (M == 0) {
         rc = cuda_status(cudaMemsetAsync(dA, 0, sizeof(float) * d->K * d->r, s), "memset dA");
@@ -811,7 +829,7 @@ int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, cons
         // as qlora_backward: the X pass beside the dX GEMM
         rc = cuda_status(cudaEventRecord(ss->fork, s), "backward fork");
         if (rc != QLORA_OK) return rc;
-        rc = gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, epilogue);
+        rc = gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, &none_or);
         const int rc_wait = cuda_status(cudaStreamWaitEvent(ss->st, ss->fork, 0), "backward fork");
         const int rc_x = rc_wait == QLORA_OK ? grad_x_ckpt(d, M, Xq, sx, dA, workspace, ss->st) : rc_wait;
         const int rc_join = cuda_status(cudaEventRecord(ss->join, ss->st), "backward join");
@@ -823,7 +841,7 @@ int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, cons
         return rc_join2;
     }
     if (dX) {
-        rc = gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, epilogue);
+        rc = gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, &none_or);
         if (rc != QLORA_OK) return rc;
     }
     return grad_x_ckpt(d, M, Xq, sx, dA, workspace, s);
