@@ -15,6 +15,10 @@ enum Act { kF32 = 0, kBF16 = 1 };
 // Xq, sx (bit-exact quantization) and xA = X . A, one pass over X.
 cudaError_t launch_quantize_rows(Act act, const void* X, const float* A, int M, int K, int r,
                                  int8_t* Xq, float* sx, float* xA, int* status, cudaStream_t s);
+// The same for qlora_forward_act: few rows and many bf16 rows in kernels of
+// their own (k1_act.cu; xA in another summation order).
+cudaError_t launch_quantize_rows_act(Act act, const void* X, const float* A, int M, int K, int r, int8_t* Xq,
+                                     float* sx, float* xA, int* status, cudaStream_t s);
 // W [K,N] fp32 -> Wq [N,K], sw [N].
 cudaError_t launch_quantize_weight(const float* W, int K, int N, int8_t* Wq, float* sw,
                                    cudaStream_t s);

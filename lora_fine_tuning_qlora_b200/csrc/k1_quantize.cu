@@ -494,16 +494,6 @@ struct StagedArgs {
     int stages_total;      // ceil(M / R)
 };
 
-// 8 bf16 (16 bytes) -> 8 floats (exact)
-__device__ __forceinline__ void bf16x8_to_f(const uint4 u, float (&f)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-}
-
 template <int TPR, int CPT, int RP>
 __global__ void __launch_bounds__(staged::cons<TPR, RP>() + 32, 1)
     k1_quantize_rows_staged_kernel(StagedArgs a, int* status) {

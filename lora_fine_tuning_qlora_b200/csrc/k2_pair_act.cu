@@ -35,10 +35,18 @@ cudaError_t launch_gemm_i8_fwd_pair_act(const int8_t* Xq, const int8_t* Wq, int 
         !make_tmap_2d(&tb, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, N, K, K, kTN / 2, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !pair_act_maps(a, ep.Y, ep.res, ep.zq, &to, &tr, &tz))
         return cudaErrorInvalidValue;
-    // epilogue warps: sixteen where the tables leave shared memory for four
-    // operand stages beside their pieces
-    if (ep.r <= 4) return launch_pair_act<4, true, 16>(ta, tb, to, tr, tz, a, status, s);
-    if (ep.r <= 8) return launch_pair_act<8, true, 16>(ta, tb, to, tr, tz, a, status, s);
+    // Short contractions are bound by the epilogue, long ones by the operand
+    // ring: sixteen epilogue warps over four stages up to K = 2048, else eight
+    // over five (us, 8192 x K x 8192 rank 4, GELU(tanh) + residual + checkpoint:
+    // K 1024: 165 against 199; 2816: 203 against 194; 4096: 254 against 237).
+    // Rank 16's tables leave no room for sixteen.
+    const bool wide = K <= 2048;
+    if (ep.r <= 4)
+        return wide ? launch_pair_act<4, true, 16>(ta, tb, to, tr, tz, a, status, s)
+                    : launch_pair_act<4, true, 8>(ta, tb, to, tr, tz, a, status, s);
+    if (ep.r <= 8)
+        return wide ? launch_pair_act<8, true, 16>(ta, tb, to, tr, tz, a, status, s)
+                    : launch_pair_act<8, true, 8>(ta, tb, to, tr, tz, a, status, s);
     return launch_pair_act<16, true, 8>(ta, tb, to, tr, tz, a, status, s);
 }
 

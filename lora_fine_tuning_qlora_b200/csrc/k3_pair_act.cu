@@ -46,15 +46,22 @@ __global__ void __launch_bounds__(kDqThreads) dequantize_kernel(const uint8_t* _
 
 }  // namespace
 
-// From how many rows the extra pass pays (measured on the 4096 x 4096 layer and
-// on a 2048 x 16384 one).
-constexpr int kDenseMinM = 1024;
+// Where the extra pass pays, in us against the kernels that de-quantize in
+// shared memory (graph replays, SILU and an added gradient): K 4096, N 4096: 512
+// rows 44 / 51, 1024 46 / 47, 4096 126 / 145, 8192 227 / 260; K 16384, N 2048:
+// 512 rows 61 / 55, 1024 88 / 100, 8192 492 / 653; K 2304, N 768: 2048 rows 20 /
+// 23.  So from 1024 rows, from 512 for kernels of up to 2^24 weights, and for
+// grids of at least 20 tiles (12 tiles: 18.9 / 18.3).
+constexpr int kDenseMinM = 1024, kDenseMinMSmall = 512;
+constexpr size_t kDenseSmall = size_t{1} << 24;
+constexpr int kDenseMinTiles = 20;
 
 size_t dx_dense_bytes(Act act, int M, int N, int K, int r) {
-    if (act != kBF16 || N % 8 != 0 || r > 16 || M < kDenseMinM) return 0;
-    const int tiles = ((M + 2 * kTM - 1) / (2 * kTM)) * ((K + kTN - 1) / kTN);
-    if (tiles < sm_count() / 4) return 0;
-    return static_cast<size_t>(N) * K * 2;
+    const size_t weights = static_cast<size_t>(N) * K;
+    if (act != kBF16 || N % 8 != 0 || r > 16) return 0;
+    if (M < (weights <= kDenseSmall ? kDenseMinMSmall : kDenseMinM)) return 0;
+    const long long tiles = static_cast<long long>((M + 2 * kTM - 1) / (2 * kTM)) * ((K + kTN - 1) / kTN);
+    return tiles >= kDenseMinTiles ? weights * 2 : 0;
 }
 
 cudaError_t launch_dequantize(const void* Wq, const float* sw, int N, int K, bool w4, void* Wd, cudaStream_t s) {

@@ -29,10 +29,16 @@
 // column yields dbias) or [G_hi | G_lo]; Bcat holds [B_hi | B_lo].  The head
 // and remainder halves sit RP = roundup(r, 16) columns apart in TMEM, so one
 // 16-column load of each gives 16 sums.
-// NT = 3 terms (the remainder of the remainder as a third table, v = hi + mid
-// + lo to 24 bits) carry the factors at fp32 precision: the dY pass of the
-// backward from 8-bit checkpoints, ranks up to 32 (beyond, the third tables do
-// not fit beside the tiles).
+//
+// NT = 3 terms (v = hi + mid + lo to 24 bits) carry the factors at fp32
+// precision: the dY pass of the backward from 8-bit checkpoints, ranks up to
+// 32 (beyond, the third tables do not fit beside the tiles).  The terms then
+// sit ceil4(r) columns apart, so that rank 4 and its ones column take one
+// 16-column MMA, and the column sums leave TMEM every kDrain tiles: the
+// tensor cores' fp32 accumulation truncates, which over the 256 products of
+// 4096 rows shrank dB by 4.4e-6 of itself; chains of 32 and fp32 additions of
+// their results (on the operand warps, from the accumulator that the next
+// group's products do not use) leave about a tenth of that.
 //
 // Column sums: the CL <= 8 CTAs that share a column block form a cluster
 // along the rows.  Each CTA owns 128/CL of the block's columns: every CTA
@@ -60,6 +66,7 @@ constexpr int kThreads = 64 + 32 * kWorkers;
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kTabSbo = (kTileCols / 8) * 128;  // 8-row group stride of a 128-wide table
 constexpr int kMaxBulkR = 8;                         // rank limit of the bulk-copied V rows
+constexpr int kDrain = 4;                            // NT = 3: tiles per column accumulator
 constexpr int kMaxPreciseR = 32;                     // rank limit of the three-term tables
 
 // What one launch computes.
@@ -86,23 +93,25 @@ struct RankTcArgs {
 // Shared-memory and TMEM layout for rank r (same on host and device).
 struct RtLayout {
     int RP, NG, NV, JP;
-    uint32_t vtab, bcat, recv, bar, vraw, vslot, total;
+    uint32_t vtab, bcat, recv, bar, vraw, vslot, drain, total;
     uint32_t tmem_cols, d_col, g_col;
     __host__ __device__ RtLayout(Parts p, int r, bool vbulk, int nt) {
-        RP = (r + 15) / 16 * 16;
-        NG = p.g ? nt * RP : 0;
-        NV = p.d ? nt * RP + (p.ones ? 16 : 0) : 0;
+        RP = nt == 3 ? (r + 3) / 4 * 4 : (r + 15) / 16 * 16;
+        NG = p.g ? (nt * RP + 15) / 16 * 16 : 0;
+        NV = p.d ? (nt * RP + (p.ones ? 1 : 0) + 15) / 16 * 16 : 0;
         JP = p.d ? r + (p.ones ? 1 : 0) : 0;
         vtab = 2 * kTileBytes;
         bcat = vtab + 2 * static_cast<uint32_t>(NV) * 256;
         recv = bcat + static_cast<uint32_t>(NG) * 256;
         bar = recv + (((kTileCols + kMaxCluster) * JP * 4 + 15) / 16) * 16;
-        vraw = bar + 128;  // [2][128 rows][r] fp32 with vbulk
+        vraw = bar + 192;  // [2][128 rows][r] fp32 with vbulk
         vslot = vbulk ? static_cast<uint32_t>(kTileRows * r * 4) : 0u;
-        total = vraw + 2 * vslot;
+        drain = vraw + 2 * vslot;  // NT = 3: the columns' sums so far, [128][JP]
+        total = drain + (nt == 3 ? static_cast<uint32_t>(kTileCols * JP * 4) : 0u);
         d_col = 0;
-        g_col = static_cast<uint32_t>(NV);
-        const uint32_t need = static_cast<uint32_t>(NV + 2 * NG);
+        const int nd = nt == 3 ? 2 * NV : NV;  // NT = 3: two column accumulators in turn
+        g_col = static_cast<uint32_t>(nd);
+        const uint32_t need = static_cast<uint32_t>(nd + 2 * NG);
         tmem_cols = 32;
         while (tmem_cols < need) tmem_cols <<= 1;
     }
@@ -136,20 +145,30 @@ __device__ __forceinline__ void put_split(uint8_t* tab, int row, int RP, int k, 
     for (int i = 0; i < NT; ++i) *reinterpret_cast<__nv_bfloat16*>(tab + ktab_off(row + i * RP, k)) = t[i];
 }
 
-// 16 sums of the NT terms' accumulators RP TMEM columns apart, smallest term
-// last in memory and added in term order.
-template <int NT>
-__device__ __forceinline__ void load_sums(uint32_t base, int RP, float (&out)[16]) {
-    uint32_t v[NT][16];
+// sink(j, sum) for the r sums of the NT terms' accumulators, RP TMEM columns apart.
+template <int NT, typename Sink>
+__device__ __forceinline__ void read_sums(uint32_t base, int RP, int r, Sink sink) {
+    if constexpr (NT == 3) {
+        for (int c0 = 0; c0 < r; c0 += 4) {
+            uint32_t v[3][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) tmem_ld16(base + i * RP, v[i]);
-    tmem_ld_wait();
+            for (int i = 0; i < 3; ++i) tmem_ld4(base + i * RP + c0, v[i]);
+            tmem_ld_wait();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        if constexpr (NT == 3)
-            out[e] = __uint_as_float(v[0][e]) + (__uint_as_float(v[1][e]) + __uint_as_float(v[2][e]));
-        else
-            out[e] = __uint_as_float(v[0][e]) + __uint_as_float(v[1][e]);
+            for (int e = 0; e < 4; ++e)
+                if (c0 + e < r)
+                    sink(c0 + e, __uint_as_float(v[0][e]) + (__uint_as_float(v[1][e]) + __uint_as_float(v[2][e])));
+        }
+    } else {
+        for (int c0 = 0; c0 < RP; c0 += 16) {
+            uint32_t hi[16], lo[16];
+            tmem_ld16(base + c0, hi);
+            tmem_ld16(base + RP + c0, lo);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (c0 + e < r) sink(c0 + e, __uint_as_float(hi[e]) + __uint_as_float(lo[e]));
+        }
     }
 }
 
@@ -169,7 +188,10 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
     uint64_t* dfull = bars + 10;  // column accumulator final
     uint64_t* rbar = bars + 11;   // every CTA of the cluster delivered this CTA's column slice
     uint64_t* vfull = bars + 12;  // [2] vbulk: the tile's V rows landed
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
+    uint64_t* dgroup = bars + 14;  // [2] NT = 3: a group's column sums are complete
+    uint64_t* dempty = bars + 16;  // [2] NT = 3: and have been read
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
+    float* drained = reinterpret_cast<float*>(smem + L.drain);  // NT = 3
     // recv[q][c][j]: partial of CTA q for column cbeg + c of this CTA's slice
     float* recv = reinterpret_cast<float*>(smem + L.recv);
 
@@ -199,6 +221,8 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
             mbar_init(&gfull[s], 1);
             mbar_init(&gempty[s], kWorkers);
             mbar_init(&vfull[s], 1);
+            mbar_init(&dgroup[s], 1);
+            mbar_init(&dempty[s], kWorkers);
         }
         mbar_init(dfull, 1);
         mbar_init(rbar, static_cast<uint32_t>(CL * (cend > cbeg ? cend - cbeg : 1)));
@@ -281,13 +305,22 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
                 }
                 if constexpr (kD) {
                     // column sums: T^T (MN-major, the two blocks 64 columns apart) x Vcat
+                    const int grp = i / kDrain;
+                    const uint32_t dcol = L.d_col + (NT == 3 ? (grp & 1) * L.NV : 0);
+                    const bool fresh = NT == 3 ? i % kDrain == 0 : i == 0;
+                    if (NT == 3 && fresh && grp >= 2 && !mbar_wait(&dempty[grp & 1], ((grp >> 1) - 1) & 1, status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kTileRows / 16; ++kk) {
                         const uint64_t ad = smem_desc(tb + kk * 2048, kBoxBytes, 1024, kLayoutSw128);
                         const uint64_t bd =
                             smem_desc(vt + s * L.NV * 256 + kk * 256, 128, kTabSbo, kLayoutNone);
-                        mma_bf16(tmem + L.d_col, ad, bd, id_d, (i > 0 || kk > 0) ? 1u : 0u);
+                        mma_bf16(tmem + dcol, ad, bd, id_d, (!fresh || kk > 0) ? 1u : 0u);
                     }
+                    if (NT == 3 && (i % kDrain == kDrain - 1 || i == nt - 1)) mma_commit(&dgroup[grp & 1]);
                 }
                 mma_commit(&empty[s]);
             }
@@ -318,7 +351,7 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    put_split<NT>(bt, j0 + e, L.RP, rr, (j0 + e < a.r && n < a.C) ? v[e] : 0.f);
+                    if (j0 + e < L.RP) put_split<NT>(bt, j0 + e, L.RP, rr, (j0 + e < a.r && n < a.C) ? v[e] : 0.f);
             }
             if constexpr (!kD) {
                 // G alone: the MMAs of the first tile wait for this table on vready[0]
@@ -335,18 +368,30 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
             const int m = (t0 + i) * kTileRows + rr;
             const uint32_t base = tmem + lane_base + L.g_col + b * L.NG;
             float* g = a.Gp + (static_cast<size_t>(cb) * a.M + m) * a.r;
-            for (int c0 = 0; c0 < L.RP; c0 += 16) {
-                float sum[16];
-                load_sums<NT>(base + c0, L.RP, sum);
-                if (m < a.M) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (c0 + e < a.r) g[c0 + e] = sum[e];
-                }
-            }
+            read_sums<NT>(base, L.RP, a.r, [&](int j, float sum) {
+                if (m < a.M) g[j] = sum;
+            });
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&gempty[b]);
+        };
+        // NT = 3: adds group g's column sums to this column's running ones
+        auto drain_group = [&](int g) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&dgroup[g & 1], (g >> 1) & 1, status));
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t base = tmem + lane_base + L.d_col + (g & 1) * L.NV;
+            float* row = drained + rr * L.JP;
+            read_sums<NT>(base, L.RP, a.r, [&](int j, float sum) { row[j] = g == 0 ? sum : row[j] + sum; });
+            if constexpr (kOnes) {
+                uint32_t ones[4];
+                tmem_ld4(base + NT * L.RP, ones);
+                tmem_ld_wait();
+                row[a.r] = g == 0 ? __uint_as_float(ones[0]) : row[a.r] + __uint_as_float(ones[0]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&dempty[g & 1]);
         };
         if constexpr (kG && !kD) {
             // the Bcat table is the only operand the workers write
@@ -455,7 +500,8 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
                             for (int e = 0; e < nv; ++e) v[e] += __ldg(p + b * stride + e);
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) put_split<NT>(vt, j0 + e, L.RP, rr, v[e]);
+                    for (int e = 0; e < 8; ++e)
+                        if (j0 + e < L.RP) put_split<NT>(vt, j0 + e, L.RP, rr, v[e]);
                 }
                 if constexpr (kOnes) {
                     const __nv_bfloat16 one = __float2bfloat16_rn(mok ? 1.f : 0.f);
@@ -471,9 +517,15 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
                 if constexpr (kG) {
                     if (i >= 1) g_epilogue(i - 1);
                 }
+                if constexpr (NT == 3) {
+                    if (ok && i >= kDrain && i % kDrain == 0) drain_group(i / kDrain - 1);
+                }
             }
             if constexpr (kG) {
                 if (ok && nt >= 1) g_epilogue(nt - 1);
+            }
+            if constexpr (NT == 3) {
+                if (ok && nt >= 1) drain_group((nt - 1) / kDrain);
             }
             // this CTA's partial of column rr goes to the CTA that owns the column
             cluster_wait();  // every CTA of the cluster has initialised its barriers
@@ -481,16 +533,12 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
             const uint32_t dst = dsmem_addr(recv + (static_cast<int>(crank) * per + rr - owner * per) * L.JP,
                                             static_cast<uint32_t>(owner));
             if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(dfull, 0, status));
-            if (ok && nt > 0) {
+            if (NT == 3 && ok && nt > 0) {
+                for (int j = 0; j < L.JP; ++j) dsmem_st(dst + 4 * j, drained[rr * L.JP + j]);
+            } else if (ok && nt > 0) {
                 tc_fence_after();
                 const uint32_t base = tmem + lane_base + L.d_col;
-                for (int c0 = 0; c0 < L.RP; c0 += 16) {
-                    float sum[16];
-                    load_sums<NT>(base + c0, L.RP, sum);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (c0 + e < a.r) dsmem_st(dst + 4 * (c0 + e), sum[e]);
-                }
+                read_sums<NT>(base, L.RP, a.r, [&](int j, float sum) { dsmem_st(dst + 4 * j, sum); });
                 if constexpr (kOnes) {
                     uint32_t ones[16];
                     tmem_ld16(base + NT * L.RP, ones);

@@ -654,6 +654,16 @@ __device__ __forceinline__ int quant_code(float v, float inv) {
     return q;
 }
 
+// 8 bf16 (16 bytes) -> 8 floats (exact)
+__device__ __forceinline__ void bf16x8_to_f(const uint4 u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
 // Symmetric abs-max codes of 8 values: rne(fl(v * inv)).  The products are
 // rounded to fp32 lane by lane (mul.rn.f32x2: two per instruction, never
 // contracted), converted with round-to-nearest-even (cvt.rni.s32.f32, on the

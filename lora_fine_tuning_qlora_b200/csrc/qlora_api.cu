@@ -413,7 +413,12 @@ int qlora_forward_act(const qlora_layer_desc* d, int M, const void* X, const int
     FwdEpilogue ep;
     rc = forward_epilogue(d, epilogue, Y, ep);
     if (rc != QLORA_OK) return rc;
-    rc = qlora_quantize_input(d, M, X, A, Xq, sx, xA, stream);
+    if (M == 0) return QLORA_OK;
+    int* status = status_ptr();
+    QL_REQUIRE(status, QLORA_ECUDA, "no CUDA device");
+    rc = cuda_status(launch_quantize_rows_act(act_of(d), X, A, M, d->K, d->r, Xq, sx, xA, status,
+                                              static_cast<cudaStream_t>(stream)),
+                     "input quantizer launch");
     if (rc != QLORA_OK) return rc;
     return gemm_forward_impl(d, M, Xq, sx, Wq, sw, bias, xA, B, Y, nullptr, 0, stream, false, epilogue);
 }
