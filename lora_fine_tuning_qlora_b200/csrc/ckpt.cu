@@ -5,11 +5,11 @@
 // read back by the same call.
 //
 // Both are bound by HBM: a bf16 element costs 2 + 1 + 1/8 bytes either way.
-// One thread takes one block (16 columns when reading back): its bytes are
-// whole 32-byte sectors, so a warp needs no exchange between threads and no
-// shared memory, and the block's maximum stays in registers.  A warp covers 8
-// rows x 4 pieces: runs of 256 bytes per row, and the 8 rows' scales, which
-// lie side by side, make one sector.
+// A lane takes 16 columns (reading back: 8) of 8 consecutive rows: neighbouring
+// lanes touch neighbouring bytes, several rows' loads are in flight together,
+// two lanes make a block (a shuffle finds its maximum), and the 8 rows' scales
+// of a block lie side by side in one sector.  At 16384 x 4096 a lane that
+// owned a whole block of one row read back in 44 us, against 33 us now.
 #include "internal.h"
 #include "ptx.cuh"
 #include "act_epilogue.cuh"
@@ -19,41 +19,145 @@ namespace qlora {
 namespace {
 
 constexpr int kCkThreads = 128;
-constexpr int kCkRows = 8, kCkPieces = 4;  // of a warp's step
+constexpr int kCkRows = 8;  // rows of a lane's step
 
-// The (row, piece) pairs of a thread: warps step through the 8 x 4 groups of
-// the matrix, along the rows first.  A pair may lie outside the matrix.
-struct Pieces {
-    size_t group, step, groups;
-    int across;
-    __device__ __forceinline__ Pieces(int rows, int pieces) {
-        across = (pieces + kCkPieces - 1) / kCkPieces;
-        groups = static_cast<size_t>((rows + kCkRows - 1) / kCkRows) * across;
-        group = blockIdx.x * static_cast<size_t>(kCkThreads / 32) + threadIdx.x / 32;
+// The steps of a thread: `chunks` 8-column chunks across, groups of 8 rows
+// down.  A warp's lanes lie along the columns (lanes_c of them, a power of
+// two of at least 4) and, for narrow matrices, over further row groups.
+struct Steps {
+    size_t at, step, total;
+    int across, lanes_c, shift, lane;
+    __device__ __forceinline__ Steps(int rows, int chunks, int lanes_log2) {
+        shift = lanes_log2;
+        lanes_c = 1 << lanes_log2;
+        lane = threadIdx.x & 31;
+        across = (chunks + lanes_c - 1) >> lanes_log2;
+        const int down = (rows + kCkRows * (32 >> lanes_log2) - 1) / (kCkRows * (32 >> lanes_log2));
+        total = static_cast<size_t>(down) * across;
+        at = blockIdx.x * static_cast<size_t>(kCkThreads / 32) + threadIdx.x / 32;
         step = static_cast<size_t>(gridDim.x) * (kCkThreads / 32);
     }
-    __device__ __forceinline__ bool next(int& row, int& piece) {
-        if (group >= groups) return false;
-        const int lane = threadIdx.x & 31;
-        const int g = static_cast<int>(group / across);
-        row = g * kCkRows + lane / kCkPieces;
-        piece = static_cast<int>(group - static_cast<size_t>(g) * across) * kCkPieces + lane % kCkPieces;
-        group += step;
+    __device__ __forceinline__ bool next(int& row0, int& chunk) {
+        if (at >= total) return false;
+        const size_t g = at / across;
+        row0 = static_cast<int>(g * (32 >> shift) + (lane >> shift)) * kCkRows;
+        chunk = static_cast<int>(at - g * across) * lanes_c + (lane & (lanes_c - 1));
+        at += step;
         return true;
     }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kCkThreads) ckpt_save_kernel(const T* __restrict__ X, int rows, int cols, int nb,
-                                                               bool vec, int8_t* __restrict__ q,
-                                                               float* __restrict__ scales) {
+// E columns (8 or 16) a lane and row; columns a multiple of E.  With 16, two
+// lanes make a block: half the divisions and shuffles per element (42 us with
+// 8 at 16384 x 4096).
+template <typename T, int E>
+__global__ void __launch_bounds__(kCkThreads) ckpt_save_kernel(const T* __restrict__ X, int rows, int cols, int lanes,
+                                                               int8_t* __restrict__ q, float* __restrict__ scales) {
+    constexpr int kSub = kCkRows / 2;              // rows whose loads are in flight together
+    constexpr int kShare = kCkptBlock / E;         // lanes of a block
     pdl_trigger();
     pdl_wait();
-    Pieces it(rows, nb);
-    for (int row, b; it.next(row, b);) {
-        if (row >= rows || b >= nb) continue;
+    const int chunks = cols / E;
+    Steps it(rows, chunks, lanes);
+    for (int row0, c; it.next(row0, c);) {
+        const bool in = c < chunks;
+        float* sc = scales + static_cast<size_t>(c / kShare) * rows + row0;
+#pragma unroll
+        for (int u0 = 0; u0 < kCkRows; u0 += kSub) {
+            RowPiece<T, E> raw[kSub];
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+                raw[u].load(X, row0 + u0 + u, in && row0 + u0 + u < rows, c * E, cols, true);
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+                float f[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) f[e] = 0.f;
+                raw[u].add_to(f);
+                uint32_t top = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) top = max(top, abs_bits(f[e]));
+#pragma unroll
+                for (int o = 1; o < kShare; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                float inv, scale;
+                ckpt_scale(top, inv, scale);
+                const int row = row0 + u0 + u;
+                if (in && row < rows) {
+                    int8_t* dst = q + static_cast<size_t>(row) * cols + c * E;
+                    uint2 w[E / 8];
+#pragma unroll
+                    for (int h = 0; h < E / 8; ++h) {
+                        float g[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) g[e] = f[8 * h + e];
+                        w[h] = codes8(g, inv);
+                    }
+                    if constexpr (E == 16) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0].x, w[0].y, w[E / 8 - 1].x, w[E / 8 - 1].y);
+                    else *reinterpret_cast<uint2*>(dst) = w[0];
+                    if (c % kShare == 0) sc[u0 + u] = scale;
+                }
+            }
+        }
+    }
+}
+
+// Columns a multiple of 8.  block 32, or 0: one scale per row.
+template <typename T>
+__global__ void __launch_bounds__(kCkThreads) ckpt_load_kernel(const int8_t* __restrict__ q,
+                                                               const float* __restrict__ scales, int rows, int cols,
+                                                               int lanes, int block, T* __restrict__ X) {
+    pdl_trigger();
+    pdl_wait();
+    const int chunks = cols / 8;
+    Steps it(rows, chunks, lanes);
+    for (int row0, c; it.next(row0, c);) {
+        if (c >= chunks) continue;
+        uint2 raw[kCkRows];
+        float s[kCkRows];
+        const float* sc = scales + (block ? static_cast<size_t>(c / 4) * rows : 0) + row0;
+#pragma unroll
+        for (int u = 0; u < kCkRows; ++u) {
+            const bool in = row0 + u < rows;
+            raw[u] = in ? __ldg(reinterpret_cast<const uint2*>(q + static_cast<size_t>(row0 + u) * cols + c * 8))
+                        : make_uint2(0u, 0u);
+            s[u] = in ? __ldg(sc + u) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kCkRows; ++u) {
+            if (row0 + u >= rows) break;
+            float v[16];
+            ckpt_values16(make_uint4(raw[u].x, raw[u].y, 0u, 0u), s[u], v);
+            uint4* dst = reinterpret_cast<uint4*>(X + static_cast<size_t>(row0 + u) * cols + c * 8);
+            if constexpr (sizeof(T) == 2) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    dst[k] = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),
+                                        __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
+            }
+        }
+    }
+}
+
+// Any column count: one thread per block and row, element by element.
+template <typename T>
+__global__ void __launch_bounds__(kCkThreads) ckpt_save_any_kernel(const T* __restrict__ X, int rows, int cols, int nb,
+                                                                   int8_t* __restrict__ q, float* __restrict__ scales) {
+    pdl_trigger();
+    pdl_wait();
+    const size_t items = static_cast<size_t>(rows) * nb;
+    for (size_t i = blockIdx.x * static_cast<size_t>(kCkThreads) + threadIdx.x; i < items;
+         i += static_cast<size_t>(gridDim.x) * kCkThreads) {
+        const int b = static_cast<int>(i / rows), row = static_cast<int>(i - static_cast<size_t>(b) * rows);
         RowPiece<T, kCkptBlock> p;
-        p.load(X, row, true, b * kCkptBlock, cols, vec);
+        p.load(X, row, true, b * kCkptBlock, cols, false);
         float v[kCkptBlock];
 #pragma unroll
         for (int e = 0; e < kCkptBlock; ++e) v[e] = 0.f;
@@ -63,66 +167,75 @@ __global__ void __launch_bounds__(kCkThreads) ckpt_save_kernel(const T* __restri
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kCkThreads) ckpt_load_kernel(const int8_t* __restrict__ q,
-                                                               const float* __restrict__ scales, int rows, int cols,
-                                                               int nc, int block, bool vec, T* __restrict__ X) {
+__global__ void __launch_bounds__(kCkThreads) ckpt_load_any_kernel(const int8_t* __restrict__ q,
+                                                                   const float* __restrict__ scales, int rows, int cols,
+                                                                   int block, T* __restrict__ X) {
     pdl_trigger();
     pdl_wait();
-    Pieces it(rows, nc);  // 16 columns each
-    for (int row, c16; it.next(row, c16);) {
-        if (row >= rows || c16 >= nc) continue;
-        const int n = c16 * 16;
-        const float scale = __ldg(scales + (block ? static_cast<size_t>(n / kCkptBlock) * rows : 0) + row);
-        const int8_t* src = q + static_cast<size_t>(row) * cols + n;
-        T* dst = X + static_cast<size_t>(row) * cols + n;
-        if (vec) {  // cols % 16 == 0
-            float v[16];
-            ckpt_values16(__ldg(reinterpret_cast<const uint4*>(src)), scale, v);
-            constexpr int kPer = 16 / static_cast<int>(sizeof(T));
-#pragma unroll
-            for (int c = 0; c < 16 / kPer; ++c) {
-                T o[kPer];
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) o[e] = ActIO<T>::from_f(v[c * kPer + e]);
-                reinterpret_cast<uint4*>(dst)[c] = *reinterpret_cast<const uint4*>(o);
-            }
-        } else {
-            for (int e = 0; e < 16 && n + e < cols; ++e)
-                dst[e] = ActIO<T>::from_f(static_cast<float>(src[e]) * scale);
-        }
+    const size_t n = static_cast<size_t>(rows) * cols;
+    for (size_t i = blockIdx.x * static_cast<size_t>(kCkThreads) + threadIdx.x; i < n;
+         i += static_cast<size_t>(gridDim.x) * kCkThreads) {
+        const size_t row = i / cols;
+        const int col = static_cast<int>(i - row * cols);
+        const float s = __ldg(scales + (block ? static_cast<size_t>(col / kCkptBlock) * rows : 0) + row);
+        X[i] = ActIO<T>::from_f(static_cast<float>(q[i]) * s);
     }
 }
 
-int ck_grid(int rows, int pieces) {
-    const size_t warps = static_cast<size_t>((rows + kCkRows - 1) / kCkRows) * ((pieces + kCkPieces - 1) / kCkPieces);
+// log2 of the lanes along the columns, at least a whole block's
+int ck_lanes(int chunks) {
+    int l = 2;
+    while (l < 5 && (1 << l) < chunks) ++l;
+    return l;
+}
+
+dim3 ck_grid(size_t warps) {
     const size_t b = (warps + kCkThreads / 32 - 1) / (kCkThreads / 32);
     const size_t cap = 16 * static_cast<size_t>(sm_count());
-    return static_cast<int>(b < 1 ? 1 : (b > cap ? cap : b));
+    return dim3(static_cast<unsigned>(b < 1 ? 1 : (b > cap ? cap : b)));
+}
+
+size_t ck_warps(int rows, int chunks, int lanes) {
+    const size_t down = (static_cast<size_t>(rows) + kCkRows * (32 >> lanes) - 1) / (kCkRows * (32 >> lanes));
+    return down * ((chunks + (1 << lanes) - 1) >> lanes);
+}
+
+template <typename T>
+cudaError_t save_t(const T* X, int rows, int cols, int8_t* q, float* scales, cudaStream_t s) {
+    if (cols % 8 == 0) {
+        const int chunks = cols % 16 == 0 ? cols / 16 : cols / 8;
+        const int lanes = ck_lanes(chunks);
+        auto kern = cols % 16 == 0 ? ckpt_save_kernel<T, 16> : ckpt_save_kernel<T, 8>;
+        return launch_k(kern, ck_grid(ck_warps(rows, chunks, lanes)), dim3(kCkThreads), 0, s, 1, X, rows, cols, lanes,
+                        q, scales);
+    }
+    const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
+    return launch_k(ckpt_save_any_kernel<T>, ck_grid((static_cast<size_t>(rows) * nb + 31) / 32), dim3(kCkThreads), 0,
+                    s, 1, X, rows, cols, nb, q, scales);
+}
+
+template <typename T>
+cudaError_t load_t(const int8_t* q, const float* scales, int rows, int cols, int block, T* X, cudaStream_t s) {
+    if (cols % 8 == 0) {
+        const int lanes = ck_lanes(cols / 8);
+        return launch_k(ckpt_load_kernel<T>, ck_grid(ck_warps(rows, cols / 8, lanes)), dim3(kCkThreads), 0, s, 1, q,
+                        scales, rows, cols, lanes, block, X);
+    }
+    return launch_k(ckpt_load_any_kernel<T>, ck_grid((static_cast<size_t>(rows) * cols + 31) / 32), dim3(kCkThreads), 0,
+                    s, 1, q, scales, rows, cols, block, X);
 }
 
 }  // namespace
 
 cudaError_t launch_ckpt_save(Act act, const void* T, int rows, int cols, int8_t* q, float* scales, cudaStream_t s) {
-    const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
-    const int grid = ck_grid(rows, nb);
-    const bool vec = cols % (act == kBF16 ? 8 : 4) == 0;
-    if (act == kBF16)
-        return launch_k(ckpt_save_kernel<__nv_bfloat16>, dim3(grid), dim3(kCkThreads), 0, s, 1,
-                        static_cast<const __nv_bfloat16*>(T), rows, cols, nb, vec, q, scales);
-    return launch_k(ckpt_save_kernel<float>, dim3(grid), dim3(kCkThreads), 0, s, 1, static_cast<const float*>(T), rows,
-                    cols, nb, vec, q, scales);
+    return act == kBF16 ? save_t(static_cast<const __nv_bfloat16*>(T), rows, cols, q, scales, s)
+                        : save_t(static_cast<const float*>(T), rows, cols, q, scales, s);
 }
 
 cudaError_t launch_ckpt_load(Act act, const int8_t* q, const float* scales, int rows, int cols, int block, void* T,
                              cudaStream_t s) {
-    const int nc = (cols + 15) / 16;
-    const int grid = ck_grid(rows, nc);
-    const bool vec = cols % 16 == 0;
-    if (act == kBF16)
-        return launch_k(ckpt_load_kernel<__nv_bfloat16>, dim3(grid), dim3(kCkThreads), 0, s, 1, q, scales, rows, cols,
-                        nc, block, vec, static_cast<__nv_bfloat16*>(T));
-    return launch_k(ckpt_load_kernel<float>, dim3(grid), dim3(kCkThreads), 0, s, 1, q, scales, rows, cols, nc, block,
-                    vec, static_cast<float*>(T));
+    return act == kBF16 ? load_t(q, scales, rows, cols, block, static_cast<__nv_bfloat16*>(T), s)
+                        : load_t(q, scales, rows, cols, block, static_cast<float*>(T), s);
 }
 
 }  // namespace qlora

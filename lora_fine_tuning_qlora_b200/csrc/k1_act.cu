@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kSplitThreads = 256;
 constexpr int kMaxS = 8;
+constexpr int kRowsThreads = 256;
 
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
@@ -148,38 +149,46 @@ __global__ void __launch_bounds__(kSplitThreads) k1_split_kernel(const T* __rest
 }
 
 // R whole rows per warp: chunk i of a lane is chunk lane + 32 i of the row.
+// A warp's next R rows arrive by one bulk copy in its own part of shared
+// memory while it computes the current ones from registers (loading straight
+// into registers, with no copy ahead, ran 62 us at 16384 x 4096).
 // A in shared memory as [pair p of a chunk's 8 rows][j / 2][chunk] of
 // (A[2p, j], A[2p+1, j], A[2p, j+1], A[2p+1, j+1]), so that neighbouring lanes
 // read neighbouring 16 bytes and a paired FMA takes two rows of A.
-template <int NCH, int RP, int R, int THREADS>
-__global__ void __launch_bounds__(THREADS) k1_rows_kernel(const __nv_bfloat16* __restrict__ X,
-                                                          const float* __restrict__ A, int M, int K, int r,
-                                                          int8_t* __restrict__ Xq, float* __restrict__ sx,
-                                                          float* __restrict__ xA) {
-    extern __shared__ float4 sA[];
+// FULL: rows of exactly 256 NCH elements.
+template <int NCH, int RP, int R, bool FULL>
+__global__ void __launch_bounds__(kRowsThreads) k1_rows_kernel(const __nv_bfloat16* __restrict__ X,
+                                                               const float* __restrict__ A, int M, int K, int r,
+                                                               int8_t* __restrict__ Xq, float* __restrict__ sx,
+                                                               float* __restrict__ xA, int* status) {
+    constexpr int kWarps = kRowsThreads / 32;
+    extern __shared__ float4 sA[];  // [4][RP / 2][nch], then the warps' rows, then their barriers
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int nch = K / 8;
+    const uint32_t row_bytes = static_cast<uint32_t>(K) * 2u;
+    uint8_t* rows = reinterpret_cast<uint8_t*>(sA + 4 * (RP / 2) * nch) + warp * R * row_bytes;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sA + 4 * (RP / 2) * nch) +
+                                                kWarps * R * row_bytes) + warp;
     pdl_trigger();
+    if (lane == 0) mbar_init(bar, 1);
+    fence_mbar_init();
+    __syncwarp();
     pdl_wait();
     const int groups = (M + R - 1) / R;
-    const int step = gridDim.x * (THREADS / 32);
-    uint4 x[R][NCH];
-    auto load = [&](int g) {
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-            const int m = g * R + q;
-            const uint4* p = reinterpret_cast<const uint4*>(X + static_cast<size_t>(m) * K);
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                const int c = lane + 32 * i;
-                x[q][i] = (m < M && c < nch) ? __ldg(p + c) : make_uint4(0u, 0u, 0u, 0u);
-            }
+    const int step = gridDim.x * kWarps;
+    auto fetch = [&](int g) {  // the group's rows into this warp's buffer
+        if (lane == 0) {
+            const uint32_t bytes = static_cast<uint32_t>(min(R, M - g * R)) * row_bytes;
+            mbar_arrive_expect_tx(bar, bytes);
+            bulk_load(rows, X + static_cast<size_t>(g) * R * K, bytes, bar);
         }
     };
-    int g = blockIdx.x * (THREADS / 32) + warp;
-    if (g < groups) load(g);
+    uint4 x[R][NCH];
+    int g = blockIdx.x * kWarps + warp;
+    if (g < groups) fetch(g);
+    uint32_t phase = 0;
     // A, while the first rows are in flight
-    for (int i = threadIdx.x; i < nch * 4 * (RP / 2); i += THREADS) {
+    for (int i = threadIdx.x; i < nch * 4 * (RP / 2); i += kRowsThreads) {
         const int c = i % nch, pj = i / nch;
         const int p = pj / (RP / 2), j = 2 * (pj % (RP / 2));
         const float* a0 = A + static_cast<size_t>(8 * c + 2 * p) * r;
@@ -190,6 +199,19 @@ __global__ void __launch_bounds__(THREADS) k1_rows_kernel(const __nv_bfloat16* _
     __syncthreads();
     const ulonglong2* sA2 = reinterpret_cast<const ulonglong2*>(sA);
     for (; g < groups; g += step) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar, phase, status))) break;
+        phase ^= 1u;
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const uint4* p = reinterpret_cast<const uint4*>(rows + q * row_bytes);
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int c = lane + 32 * i;
+                x[q][i] = (g * R + q < M && (FULL || c < nch)) ? p[c] : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        __syncwarp();
+        if (g + step < groups) fetch(g + step);
         float inv[R];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
@@ -214,7 +236,7 @@ __global__ void __launch_bounds__(THREADS) k1_rows_kernel(const __nv_bfloat16* _
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const int c = lane + 32 * i;
-            const bool in = c < nch;
+            const bool in = FULL || c < nch;
             float f[R][8];
 #pragma unroll
             for (int q = 0; q < R; ++q) {
@@ -230,7 +252,7 @@ __global__ void __launch_bounds__(THREADS) k1_rows_kernel(const __nv_bfloat16* _
                 for (int q = 0; q < R; ++q) x2[q] = pk2(f[q][2 * p], f[q][2 * p + 1]);
 #pragma unroll
                 for (int j2 = 0; j2 < RP / 2; ++j2) {
-                    const ulonglong2 a = sA2[(p * (RP / 2) + j2) * nch + cs];
+                    const ulonglong2 a = sA2[(p * (RP / 2) + j2) * (FULL ? 32 * NCH : nch) + cs];
 #pragma unroll
                     for (int q = 0; q < R; ++q) {
                         fma2(acc[q][2 * j2], x2[q], a.x);
@@ -239,7 +261,6 @@ __global__ void __launch_bounds__(THREADS) k1_rows_kernel(const __nv_bfloat16* _
                 }
             }
         }
-        if (g + step < groups) load(g + step);
         constexpr int V = R * RP;
         float v[V];
 #pragma unroll
@@ -270,17 +291,19 @@ cudaError_t launch_split(const T* X, const float* A, int M, int K, int r, int8_t
     return launch_k(k1_split_kernel<T, RP>, dim3(M, S), dim3(kSplitThreads), 0, s, S, X, A, K, r, vec, Xq, sx, xA);
 }
 
-template <int NCH, int RP, int R, int THREADS>
+template <int NCH, int RP, int R>
 cudaError_t launch_rows(const __nv_bfloat16* X, const float* A, int M, int K, int r, int8_t* Xq, float* sx, float* xA,
-                        int per_sm, cudaStream_t s) {
-    auto kern = k1_rows_kernel<NCH, RP, R, THREADS>;
-    const int smem = K / 8 * 4 * (RP / 2) * 16;
+                        int per_sm, int* status, cudaStream_t s) {
+    constexpr int kWarps = kRowsThreads / 32;
+    auto kern = K == 256 * NCH ? k1_rows_kernel<NCH, RP, R, true> : k1_rows_kernel<NCH, RP, R, false>;
+    const int smem = K / 8 * 4 * (RP / 2) * 16 + kWarps * R * K * 2 + kWarps * 8;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     const int groups = (M + R - 1) / R;
-    const int ctas = (groups + THREADS / 32 - 1) / (THREADS / 32);
+    const int ctas = (groups + kWarps - 1) / kWarps;
     const int cap = per_sm * sm_count();
-    return launch_k(kern, dim3(ctas < cap ? ctas : cap), dim3(THREADS), smem, s, 1, X, A, M, K, r, Xq, sx, xA);
+    return launch_k(kern, dim3(ctas < cap ? ctas : cap), dim3(kRowsThreads), smem, s, 1, X, A, M, K, r, Xq, sx, xA,
+                    status);
 }
 
 }  // namespace
@@ -299,15 +322,20 @@ cudaError_t launch_quantize_rows_act(Act act, const void* X, const float* A, int
         if (r <= 8) return launch_split<float, 8>(xf, A, M, K, r, Xq, sx, xA, s);
         return launch_split<float, 16>(xf, A, M, K, r, Xq, sx, xA, s);
     }
+    // us against the kernels there: 16384 x 4096 47 / 68, 16384 x 2048 29 / 46,
+    // 8192 x 4096 31 / 39, but 4096 x 2048 15 / 12: from 2^24 elements.  Two
+    // CTAs per SM where A and the rows fit twice.
+    if (static_cast<long long>(M) * K < (1LL << 24))
+        return launch_quantize_rows(act, X, A, M, K, r, Xq, sx, xA, status, s);
     if (act == kBF16 && r <= 4 && K <= 4096) {
-        if (K <= 1024) return launch_rows<4, 4, 2, 256>(xb, A, M, K, r, Xq, sx, xA, 3, s);
-        if (K <= 2048) return launch_rows<8, 4, 2, 256>(xb, A, M, K, r, Xq, sx, xA, 2, s);
-        return launch_rows<16, 4, 2, 384>(xb, A, M, K, r, Xq, sx, xA, 1, s);
+        if (K <= 1024) return launch_rows<4, 4, 2>(xb, A, M, K, r, Xq, sx, xA, 2, status, s);
+        if (K <= 2048) return launch_rows<8, 4, 2>(xb, A, M, K, r, Xq, sx, xA, 2, status, s);
+        return launch_rows<16, 4, 2>(xb, A, M, K, r, Xq, sx, xA, 1, status, s);
     }
     if (act == kBF16 && r <= 8 && K <= 4096) {
-        if (K <= 1024) return launch_rows<4, 8, 2, 256>(xb, A, M, K, r, Xq, sx, xA, 2, s);
-        if (K <= 2048) return launch_rows<8, 8, 2, 256>(xb, A, M, K, r, Xq, sx, xA, 2, s);
-        return launch_rows<16, 8, 1, 384>(xb, A, M, K, r, Xq, sx, xA, 1, s);
+        if (K <= 1024) return launch_rows<4, 8, 2>(xb, A, M, K, r, Xq, sx, xA, 2, status, s);
+        if (K <= 2048) return launch_rows<8, 8, 1>(xb, A, M, K, r, Xq, sx, xA, 2, status, s);
+        return launch_rows<16, 8, 1>(xb, A, M, K, r, Xq, sx, xA, 1, status, s);
     }
     return launch_quantize_rows(act, X, A, M, K, r, Xq, sx, xA, status, s);
 }

@@ -10,6 +10,7 @@ PyTorch only provides device memory and streams here.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -669,23 +670,31 @@ def _expect(t, name: str, shape, dtype, device):
     """Checks one tensor argument; returns its address (None for None)."""
     if t is None:
         return None
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape or t.dtype != dtype:
         raise ValueError("%s must be %s of shape %s" % (name, dtype, tuple(shape)))
     if t.device != device:
         raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _on_device(t: torch.Tensor, what: str, stream):
-    """The stream's handle; the library works on the current device, so the
-    tensors have to be there."""
+    """(device, stream handle) of a call on t: the library works on the current
+    device, so the tensors have to be there."""
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % what)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d" % (what, t.device, torch.cuda.current_device()))
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    dev = t.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (what, dev, torch.cuda.current_device()))
+    if stream is not None:
+        return dev, stream.cuda_stream
+    return dev, torch._C._cuda_getCurrentRawStream(dev.index)  # current_stream() without its object
+
+
+def _allocating_on(stream):
+    """Outputs are allocated on the stream that writes them."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
 def ckpt_buffers(M: int, N: int, device=None):
@@ -704,8 +713,7 @@ def ckpt_workspace(d: LayerDesc, M: int, device=None) -> torch.Tensor:
 
 
 def _check_layer_tensors(layer: "Layer", dev):
-    K, N, r = layer.K, layer.N, layer.r
-    f32 = torch.float32
+    (N, K), r, f32 = layer.Wq.shape, layer.A.shape[1], torch.float32
     return (_expect(layer.Wq, "Wq", (N, K), torch.int8, dev), _expect(layer.sw, "sw", (N,), f32, dev),
             _expect(layer.bias, "bias", (N,), f32, dev), _expect(layer.A, "A", (K, r), f32, dev),
             _expect(layer.B, "B", (r, N), f32, dev))
@@ -720,17 +728,18 @@ def forward_act(layer: Layer, X: torch.Tensor, act: str = "none", residual: Opti
     bits); ``keep`` gives its buffers, else they are allocated.  ``residual``
     may be ``Y`` itself.  Gradients: ``backward_ckpt``."""
     fn = act_fn(act)
-    s = _on_device(X, "X", stream)
-    dev, M, K, N, r = X.device, X.shape[0], layer.K, layer.N, layer.r
+    dev, s = _on_device(X, "X", stream)
+    M, (N, K), r = X.shape[0], layer.Wq.shape, layer.A.shape[1]
     x = _expect(X, "X", (M, K), layer.act, dev)
     wq, sw, bias, a, b = _check_layer_tensors(layer, dev)
-    if Y is None:
-        Y = torch.empty((M, N), dtype=layer.act, device=dev)
-    if keep is None:
-        zq, zs = ckpt_buffers(M, N, dev) if save_z else (None, None)
-        keep = Checkpoint(torch.empty((M, K), dtype=torch.int8, device=dev),
-                          torch.empty((M,), dtype=torch.float32, device=dev),
-                          torch.empty((M, r), dtype=torch.float32, device=dev), zq, zs)
+    with _allocating_on(stream):
+        if Y is None:
+            Y = torch.empty((M, N), dtype=layer.act, device=dev)
+        if keep is None:
+            zq, zs = ckpt_buffers(M, N, dev) if save_z else (None, None)
+            keep = Checkpoint(torch.empty((M, K), dtype=torch.int8, device=dev),
+                              torch.empty((M,), dtype=torch.float32, device=dev),
+                              torch.empty((M, r), dtype=torch.float32, device=dev), zq, zs)
     if save_z and keep.zq is None:
         raise ValueError("save_z needs zq and zs in keep")
     f32 = torch.float32
@@ -766,27 +775,28 @@ def backward_ckpt(layer: Layer, keep: Checkpoint, dY: torch.Tensor, ws: torch.Te
     activation that produced this layer's input: dX is taken back through it.
     ``add`` is added to dX (the gradient of a skip connection; it may be ``dX``
     itself).  ``ws``: ``ckpt_workspace``."""
-    s = _on_device(dY, "dY", stream)
-    dev, M, K, N, r = dY.device, dY.shape[0], layer.K, layer.N, layer.r
+    dev, s = _on_device(dY, "dY", stream)
+    M, (N, K), r = dY.shape[0], layer.Wq.shape, layer.A.shape[1]
     f32 = torch.float32
     dy = _expect(dY, "dY", (M, N), layer.act, dev)
     wq, sw, _, a, b = _check_layer_tensors(layer, dev)
     xq, sx = _expect(keep.Xq, "Xq", (M, K), torch.int8, dev), _expect(keep.sx, "sx", (M,), f32, dev)
     xa = _expect(keep.xA, "xA", (M, r), f32, dev)
     ep = _dx_epilogue(act, z, add, M, K, layer.act, dev)
-    if not want_dx:
-        dX = None
-    elif dX is None:
-        dX = torch.empty((M, K), dtype=layer.act, device=dev)
     w = _expect(ws, "ws", ws.shape, torch.uint8, dev)
-    dA = torch.empty((K, r), dtype=f32, device=dev)
-    dB = torch.empty((r, N), dtype=f32, device=dev)
-    dbias = torch.empty((N,), dtype=f32, device=dev) if want_dbias else None
-    if M == 0:
-        for g in (dA, dB, dbias):
-            if g is not None:
-                g.zero_()
-        return dX, dA, dB, dbias
+    with _allocating_on(stream):
+        if not want_dx:
+            dX = None
+        elif dX is None:
+            dX = torch.empty((M, K), dtype=layer.act, device=dev)
+        dA = torch.empty((K, r), dtype=f32, device=dev)
+        dB = torch.empty((r, N), dtype=f32, device=dev)
+        dbias = torch.empty((N,), dtype=f32, device=dev) if want_dbias else None
+        if M == 0:
+            for g in (dA, dB, dbias):
+                if g is not None:
+                    g.zero_()
+            return dX, dA, dB, dbias
     _check(_lib.qlora_backward_ckpt(layer.desc(), M, xq, sx, dy, wq, sw, a, b, xa, ep,
                                     _expect(dX, "dX", (M, K), layer.act, dev), dA.data_ptr(), dB.data_ptr(),
                                     dbias.data_ptr() if want_dbias else None, w, ws.numel(), s))
@@ -827,15 +837,18 @@ def qlora_lora_grad_x_ckpt(d: LayerDesc, M: int, Xq, sx, dA, ws, stream=None):
 
 def ckpt_save(T: torch.Tensor, out=None, stream=None):
     """The 8-bit checkpoint (q [M, N], scales [ceil(N / 32), M]) of T [M, N]."""
-    s = _on_device(T, "T", stream)
+    dev, s = _on_device(T, "T", stream)
     if T.dim() != 2:
         raise ValueError("T must have two axes")
     M, N = T.shape
-    q, scales = out if out is not None else ckpt_buffers(M, N, T.device)
-    _check(_lib.qlora_ckpt_save(_expect(T, "T", (M, N), T.dtype, T.device), M, N, act_code(T.dtype),
-                                _expect(q, "q", (M, N), torch.int8, T.device),
-                                _expect(scales, "scales", (-(-N // CKPT_BLOCK), M), torch.float32, T.device),
-                                s) if M > 0 else 0)
+    if out is None:
+        with _allocating_on(stream):
+            out = ckpt_buffers(M, N, dev)
+    q, scales = out
+    args = (_expect(T, "T", (M, N), T.dtype, dev), M, N, act_code(T.dtype), _expect(q, "q", (M, N), torch.int8, dev),
+            _expect(scales, "scales", (-(-N // CKPT_BLOCK), M), torch.float32, dev), s)
+    if M > 0:
+        _check(_lib.qlora_ckpt_save(*args))
     return q, scales
 
 
@@ -843,15 +856,17 @@ def ckpt_load(q: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of codes q [M, N]: with scales [ceil(N / 32), M] of an 8-bit
     checkpoint, or [M] of row codes (Xq, sx)."""
-    s = _on_device(q, "q", stream)
+    dev, s = _on_device(q, "q", stream)
     if q.dim() != 2:
         raise ValueError("q must have two axes")
     M, N = q.shape
     block = 0 if scales.dim() == 1 else CKPT_BLOCK
-    T = out if out is not None else torch.empty((M, N), dtype=dtype, device=q.device)
+    if out is None:
+        with _allocating_on(stream):
+            out = torch.empty((M, N), dtype=dtype, device=dev)
     shape = (M,) if block == 0 else (-(-N // CKPT_BLOCK), M)
-    _check(_lib.qlora_ckpt_load(_expect(q, "q", (M, N), torch.int8, q.device),
-                                _expect(scales, "scales", shape, torch.float32, q.device), M, N, block,
-                                act_code(T.dtype), _expect(T, "out", (M, N), T.dtype, q.device),
-                                s) if M > 0 else 0)
-    return T
+    args = (_expect(q, "q", (M, N), torch.int8, dev), _expect(scales, "scales", shape, torch.float32, dev), M, N, block,
+            act_code(out.dtype), _expect(out, "out", (M, N), out.dtype, dev), s)
+    if M > 0:
+        _check(_lib.qlora_ckpt_load(*args))
+    return out
