@@ -118,10 +118,12 @@ cudaError_t launch_quantize_outlier(const float* W, int K, int N, const OutlierK
 cudaError_t launch_gemm_dx(Act act, const void* dY, const int8_t* Wq, const float* sw, int M,
                            int N, int K, const DxEpilogue& ep, int* status, cudaStream_t s,
                            bool w4 = false);
-// Its large-tile (tc) or CUDA-core kernels with the EX epilogue (k3_dx_act.cu);
-// mode 0 int8 codes, 1 packed int4.
-cudaError_t launch_gemm_dx_act(Act act, bool tc, const void* dY, const int8_t* Wq, const float* sw, int M, int N,
-                               int K, const DxEpilogue& ep, int* status, cudaStream_t s, int mode);
+// Its large-tile kernels with the EX epilogue (k3_dx_act.cu; mode 0 int8 codes,
+// 1 packed int4), and the CUDA-core kernel with it (k3_simt_act.cu).
+cudaError_t launch_gemm_dx_act(const void* dY, const int8_t* Wq, const float* sw, int M, int N, int K,
+                               const DxEpilogue& ep, int* status, cudaStream_t s, int mode);
+cudaError_t launch_gemm_dx_simt_act(Act act, const void* dY, const int8_t* Wq, const float* sw, int M, int N, int K,
+                                    const DxEpilogue& ep, cudaStream_t s, bool w4);
 // The bf16 dX GEMM on CTA pairs (256 x 256 tiles, k3_dx_pair.cu): for N a
 // multiple of 64, rank <= 16 and at least one wave of pair tiles.
 bool gemm_dx_pair_applies(int M, int N, int K, int r);

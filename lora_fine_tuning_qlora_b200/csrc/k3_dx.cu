@@ -9,13 +9,13 @@ cudaError_t launch_gemm_dx(Act act, const void* dY, const int8_t* Wq, const floa
     const bool tc = act == kBF16 && (N % 8) == 0 && (!ep.ol.par || (K % 16) == 0);
     const int mode = ep.ol.par ? 2 : (w4 ? 1 : 0);
     if (!tc)
-        return ep.ex ? launch_gemm_dx_act(act, false, dY, Wq, sw, M, N, K, ep, status, s, mode)
-                     : launch_gemm_dx_simt<false>(act, dY, Wq, sw, M, N, K, ep, s, mode);
+        return ep.ex ? launch_gemm_dx_simt_act(act, dY, Wq, sw, M, N, K, ep, s, w4)
+                     : launch_gemm_dx_simt(act, dY, Wq, sw, M, N, K, ep, s, mode);
     if (mode != 2 && !ep.bias && small_m_applies(M, K, ep.r))
         return launch_gemm_dx_small(dY, Wq, sw, M, N, K, ep, status, s, w4);
     if (gemm_dx_pair_applies(M, N, K, ep.r))
         return launch_gemm_dx_pair(dY, Wq, sw, M, N, K, ep, status, s, w4);
-    return ep.ex ? launch_gemm_dx_act(act, true, dY, Wq, sw, M, N, K, ep, status, s, mode)
+    return ep.ex ? launch_gemm_dx_act(dY, Wq, sw, M, N, K, ep, status, s, mode)
                  : launch_gemm_dx_tiles<false>(dY, Wq, sw, M, N, K, ep, status, s, mode);
 }
 

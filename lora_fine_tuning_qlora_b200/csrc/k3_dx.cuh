@@ -576,7 +576,7 @@ cudaError_t launch_tc_r(int cfg, const void* dY, const int8_t* Wq, const float* 
 constexpr int kSB = 64;
 constexpr int kSN = 16;
 
-template <typename T, int MODE, bool EX>
+template <typename T, int MODE>
 __global__ void __launch_bounds__(256) k3_dx_simt_kernel(const T* __restrict__ dY,
                                                          const int8_t* __restrict__ Wq,
                                                          const float* __restrict__ sw, int M,
@@ -670,41 +670,26 @@ __global__ void __launch_bounds__(256) k3_dx_simt_kernel(const T* __restrict__ d
             const bool pass =
                 !ep.gate || ActIO<T>::to_f(static_cast<const T*>(ep.gate)[static_cast<size_t>(m) * K + k]) > 0.f;
             const float b = ep.bias ? __ldg(ep.bias + k) : 0.f;
-            if constexpr (EX) {
-                float y[1] = {acc[i][j] + ep.c * l};
-                if (ep.act != kActNone) {
-                    const float z[1] = {static_cast<float>(ep.zq[static_cast<size_t>(m) * K + k]) *
-                                        __ldg(ep.zs + static_cast<size_t>(k / kCkptBlock) * M + m)};
-                    slope_apply(ep.act, z, y);
-                }
-                if (ep.add) y[0] += ActIO<T>::to_f(static_cast<const T*>(ep.add)[static_cast<size_t>(m) * K + k]);
-                dX[static_cast<size_t>(m) * K + k] = ActIO<T>::from_f(y[0]);
-                continue;
-            }
             dX[static_cast<size_t>(m) * K + k] = ActIO<T>::from_f(pass ? acc[i][j] + ep.c * l + b : 0.f);
         }
     }
 }
 
-// The CUDA-core kernel for one epilogue form.
-template <bool EX>
-cudaError_t launch_gemm_dx_simt(Act act, const void* dY, const int8_t* Wq, const float* sw, int M, int N, int K,
-                                const DxEpilogue& ep, cudaStream_t s, int mode) {
+// The CUDA-core kernel with the plain epilogue.
+inline cudaError_t launch_gemm_dx_simt(Act act, const void* dY, const int8_t* Wq, const float* sw, int M, int N, int K,
+                                       const DxEpilogue& ep, cudaStream_t s, int mode) {
     dim3 grid((K + kSB - 1) / kSB, (M + kSB - 1) / kSB);
     auto run = [&](auto kern, auto* dy) {
         return launch_k(kern, grid, dim3(256), 0, s, 1, dy, Wq, sw, M, N, K, ep);
     };
     if (act == kBF16) {
         const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(dY);
-        if constexpr (!EX)
-            if (mode == 2) return run(k3_dx_simt_kernel<__nv_bfloat16, 2, false>, dy);
-        return mode == 1 ? run(k3_dx_simt_kernel<__nv_bfloat16, 1, EX>, dy)
-                         : run(k3_dx_simt_kernel<__nv_bfloat16, 0, EX>, dy);
+        if (mode == 2) return run(k3_dx_simt_kernel<__nv_bfloat16, 2>, dy);
+        return mode == 1 ? run(k3_dx_simt_kernel<__nv_bfloat16, 1>, dy) : run(k3_dx_simt_kernel<__nv_bfloat16, 0>, dy);
     }
     const float* dy = static_cast<const float*>(dY);
-    if constexpr (!EX)
-        if (mode == 2) return run(k3_dx_simt_kernel<float, 2, false>, dy);
-    return mode == 1 ? run(k3_dx_simt_kernel<float, 1, EX>, dy) : run(k3_dx_simt_kernel<float, 0, EX>, dy);
+    if (mode == 2) return run(k3_dx_simt_kernel<float, 2>, dy);
+    return mode == 1 ? run(k3_dx_simt_kernel<float, 1>, dy) : run(k3_dx_simt_kernel<float, 0>, dy);
 }
 
 // The large-tile tensor-core kernels of this file for one epilogue form.

@@ -25,6 +25,9 @@
 // Rows are split over a cluster of CL <= 8 CTAs per 128-column block, whose
 // partial sums meet in the shared memory of the CTA that owns the column, as
 // int64.  Warps: 0 producer, 1 TMEM owner and MMA issuer, 2..5 read-out.
+//
+// Up to 128 rows (one tile) there is no digit kernel: warps 2..5 of every CTA
+// make the tile's table themselves, a launch less.
 #include "internal.h"
 #include "ptx.cuh"
 #include "tile_epilogue.cuh"
@@ -52,6 +55,23 @@ constexpr int kExpNaN = -0x40000000;  // the column holds an infinity or a NaN
 // Byte offset of digit row n (= digit * ceil4(r) + j) of tile row k.
 __device__ __forceinline__ uint32_t digit_off(int n, int k) {
     return static_cast<uint32_t>((n >> 3) * kSbo + (k >> 4) * 128 + (n & 7) * 16 + (k & 15));
+}
+
+// The exponent p of a column whose largest magnitude has the bits `top`: top <
+// 2^(E - 126) for its biased exponent E, so V 2^(156 - E) < 2^30.
+__device__ __forceinline__ int column_exponent(uint32_t top) {
+    const int E = static_cast<int>(top >> 23);
+    return top >= 0x7F800000u ? kExpNaN : (top == 0u ? 0 : 156 - (E > 0 ? E : 1));
+}
+
+// The four digits of v 2^p, lowest first.
+__device__ __forceinline__ void make_digits(float v, int p, int (&d)[4]) {
+    int t = __float2int_rn(scalbnf(v, p));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        d[i] = i < 3 ? static_cast<int>(static_cast<int8_t>(t & 0xFF)) : t;
+        t = (t - d[i]) >> 8;
+    }
 }
 
 // One cluster.  Two sweeps over G: the columns' maxima of |V|, then the
@@ -86,9 +106,7 @@ __global__ void __launch_bounds__(kPrepThreads) k4_q_digits_kernel(const float* 
     if (tid < 64) {
         uint32_t t = 0;
         for (uint32_t q = 0; q < CL; ++q) t = max(t, dsmem_ld_u32(dsmem_addr(&top[tid], q)));
-        // t < 2^(E - 126) for a biased exponent E, so V 2^(156 - E) < 2^30
-        const int E = static_cast<int>(t >> 23);
-        const int p = t >= 0x7F800000u ? kExpNaN : (t == 0u ? 0 : 156 - (E > 0 ? E : 1));
+        const int p = column_exponent(t);
         pexp[tid] = p;
         if (rank == 0) reinterpret_cast<int*>(digits)[tid] = p;
     }
@@ -108,13 +126,10 @@ __global__ void __launch_bounds__(kPrepThreads) k4_q_digits_kernel(const float* 
             for (int e = 0; e < 4; ++e) {
                 const size_t m = tile * kRows + 4 * g + e;
                 if (m >= static_cast<size_t>(M)) continue;
-                int t = __float2int_rn(scalbnf(value(m, j), p));
+                int dg[4];
+                make_digits(value(m, j), p, dg);
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const int c = d < 3 ? static_cast<int>(static_cast<int8_t>(t & 0xFF)) : t;
-                    w[d] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * e);
-                    t = (t - c) >> 8;
-                }
+                for (int d = 0; d < 4; ++d) w[d] |= (static_cast<uint32_t>(dg[d]) & 0xFFu) << (8 * e);
             }
         }
         uint8_t* tab = digits + kExpBytes + tile * (static_cast<size_t>(4 * RP) * kRows);
@@ -128,7 +143,10 @@ __global__ void __launch_bounds__(kPrepThreads) k4_q_digits_kernel(const float* 
 }
 
 struct RankQArgs {
-    const uint8_t* digits;
+    const uint8_t* digits;  // null: one tile, whose digits the kernel makes itself from
+    const float* G;         // the nsl slices of G and sx
+    int nsl;
+    const float* sx;
     float* dA;
     int M, K, r;
     int tiles_per_cta;
@@ -145,7 +163,7 @@ struct RqLayout {
         stage = kTileBytes + static_cast<uint32_t>(NV) * kRows;
         recv = static_cast<uint32_t>(stages) * stage;
         bar = recv + static_cast<uint32_t>((kCols + kMaxCl) * r * 8);
-        total = bar + (2 * kMaxStages + 4) * 8;
+        total = bar + (2 * kMaxStages + 4) * 8;  // full, empty, dfull, rbar, vready, TMEM address
         tmem_cols = 32;
         while (tmem_cols < static_cast<uint32_t>(NV)) tmem_cols <<= 1;
     }
@@ -162,7 +180,11 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
     uint64_t* empty = full + kMaxStages;
     uint64_t* dfull = empty + kMaxStages;
     uint64_t* rbar = dfull + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + 1);
+    uint64_t* vready = rbar + 1;  // without a digits buffer: the table is written
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vready + 1);
+    __shared__ uint32_t s_top[64];
+    __shared__ int s_exp[64];
+    const bool own = a.digits == nullptr;
     // recv[q][c][j]: the sums of CTA q for column cbeg + c of this CTA's slice
     long long* recv = reinterpret_cast<long long*>(smem + L.recv);
     uint32_t CL;
@@ -183,9 +205,11 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
             mbar_init(&empty[s], 1);
         }
         mbar_init(dfull, 1);
+        mbar_init(vready, 4);
         mbar_init(rbar, static_cast<uint32_t>(static_cast<int>(CL) * max(1, cend - cbeg)));
         fence_mbar_init();
     }
+    if (threadIdx.x < 64) s_top[threadIdx.x] = 0u;
     if (warp == 1) {
         tmem_alloc(tmem_slot, L.tmem_cols);
         tmem_relinquish();
@@ -201,14 +225,14 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
         if (lane == 0) {
             tma_prefetch_desc(&tmX);
             const uint32_t tab = static_cast<uint32_t>(L.NV) * kRows;
-            const uint8_t* src = a.digits + kExpBytes;
+            const uint8_t* src = own ? nullptr : a.digits + kExpBytes;
             for (int i = 0; i < nt; ++i) {
                 const int s = i % S;
                 if (i >= S && !mbar_wait(&empty[s], ((i / S) - 1) & 1, status)) break;
                 uint8_t* st = smem + s * L.stage;
-                mbar_arrive_expect_tx(&full[s], L.stage);
+                mbar_arrive_expect_tx(&full[s], own ? kTileBytes : L.stage);
                 tma_load_2d(st, &tmX, &full[s], col0, (t0 + i) * kRows);
-                bulk_load(st + kTileBytes, src + static_cast<size_t>(t0 + i) * tab, tab, &full[s]);
+                if (!own) bulk_load(st + kTileBytes, src + static_cast<size_t>(t0 + i) * tab, tab, &full[s]);
             }
         }
         __syncwarp();
@@ -219,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
             bool ok = true;
             for (int i = 0; i < nt; ++i) {
                 const int s = i % S;
-                if (!mbar_wait(&full[s], (i / S) & 1, status)) {
+                if (!mbar_wait(&full[s], (i / S) & 1, status) || (own && !mbar_wait(vready, 0, status))) {
                     ok = false;
                     break;
                 }
@@ -241,6 +265,32 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
         __syncwarp();
         cluster_wait();
     } else {
+        if (own) {
+            // the one tile's table (stage 0): thread = row
+            const int m = threadIdx.x - 64;
+            const size_t n = static_cast<size_t>(a.M) * a.r;
+            const float sxm = m < a.M ? __ldg(a.sx + m) : 0.f;
+            auto value = [&](int j) {
+                return m < a.M ? sum_slices(a.G + static_cast<size_t>(m) * a.r + j, n, a.nsl) * sxm : 0.f;
+            };
+            for (int j = 0; j < a.r; ++j) {
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(value(j)) & 0x7FFFFFFFu);
+                if (lane == 0) atomicMax(&s_top[j], top);
+            }
+            named_bar_sync(1, 128);
+            if (m < 64) s_exp[m] = column_exponent(s_top[m]);
+            named_bar_sync(1, 128);
+            uint8_t* tab = smem + kTileBytes;
+            for (int j = 0; j < L.RP; ++j) {
+                int d[4] = {0, 0, 0, 0};
+                if (j < a.r && s_exp[j] != kExpNaN) make_digits(value(j), s_exp[j], d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tab[digit_off(i * L.RP + j, m)] = static_cast<uint8_t>(d[i]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(vready);
+        }
         cluster_wait();  // every CTA of the cluster has initialised its barriers
         const int wq = warp & 3;
         const int rr = wq * 32 + lane;  // column of the block
@@ -284,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
     // touches this CTA's shared memory from outside
     const int width = cend - cbeg;
     if (width > 0 && mbar_wait_cluster(rbar, 0, status)) {
-        const int* pexp = reinterpret_cast<const int*>(a.digits);
+        const int* pexp = own ? s_exp : reinterpret_cast<const int*>(a.digits);
         for (int idx = threadIdx.x; idx < width * a.r; idx += kThreads) {
             const int cc = idx / a.r, j = idx - cc * a.r;
             const int col = col0 + cbeg + cc;
@@ -292,7 +342,7 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
             long long sum = 0;
             for (int q = 0; q < static_cast<int>(CL); ++q)
                 sum += recv[static_cast<size_t>(q * per + cc) * a.r + j];
-            const int p = __ldg(pexp + j);
+            const int p = pexp[j];
             const double v = p == kExpNaN ? __longlong_as_double(0x7FF8000000000000LL)
                                           : scalbn(static_cast<double>(sum), -p) * static_cast<double>(a.c);
             a.dA[static_cast<size_t>(col) * a.r + j] = static_cast<float>(v);
@@ -309,18 +359,25 @@ size_t rank_q_digit_bytes(int M, int r) {
 cudaError_t launch_rank_x_q(const int8_t* Xq, const float* sx, const float* G, int nsl, int M, int K, int r,
                             float c, void* digits, float* dA, int* status, cudaStream_t s) {
     if (M > kRankQMaxRows) return cudaErrorInvalidValue;
-    // digits: a cluster of CTAs, about 8 elements a thread
-    const size_t n = static_cast<size_t>(M) * r;
-    int pc = 1;
-    while (pc < 8 && n > static_cast<size_t>(pc) * kPrepThreads * 8) pc *= 2;
-    cudaError_t e = launch_k(k4_q_digits_kernel, dim3(1, pc), dim3(kPrepThreads), 0, s, pc, G, nsl, sx, M, r,
-                             static_cast<uint8_t*>(digits));
-    if (e != cudaSuccess) return e;
+    const bool own = M <= kRows;
+    cudaError_t e = cudaSuccess;
+    if (!own) {
+        // digits: a cluster of CTAs, about 8 elements a thread
+        const size_t n = static_cast<size_t>(M) * r;
+        int pc = 1;
+        while (pc < 8 && n > static_cast<size_t>(pc) * kPrepThreads * 8) pc *= 2;
+        e = launch_k(k4_q_digits_kernel, dim3(1, pc), dim3(kPrepThreads), 0, s, pc, G, nsl, sx, M, r,
+                     static_cast<uint8_t*>(digits));
+        if (e != cudaSuccess) return e;
+    }
     CUtensorMap tm;
     if (!make_tmap_2d(&tm, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, M, K, K, kRows, kCols, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     RankQArgs a{};
-    a.digits = static_cast<const uint8_t*>(digits);
+    a.digits = own ? nullptr : static_cast<const uint8_t*>(digits);
+    a.G = G;
+    a.nsl = nsl;
+    a.sx = sx;
     a.dA = dA;
     a.M = M;
     a.K = K;
