@@ -486,27 +486,34 @@ int qlora_forward_act(const qlora_layer_desc* d, int M, const void* X, const int
                       void* Y, int8_t* Xq, float* sx, float* xA, void* stream);
 
 /* a4 with act'(z) and an added gradient: dX = (dY (Wq * sw)^T + c G A^T) *
- * act'(z) + add, G from the workspace that a3 filled, as qlora_gemm_dx. */
+ * act'(z) + add, G from the workspace that a3 filled, as qlora_gemm_dx.  In a
+ * workspace of qlora_ckpt_workspace_bytes the kernels of large bf16 layers are
+ * de-quantized once, into the part behind qlora_workspace_bytes, instead of
+ * tile by tile in shared memory (the same values, the same sums but for their
+ * fp32 grouping); a smaller one (qlora_workspace_bytes) keeps to the latter. */
 int qlora_gemm_dx_act(const qlora_layer_desc* d, int M, const void* dY, const int8_t* Wq, const float* sw,
-                      const float* A, const qlora_dx_epilogue* epilogue, void* dX, const void* workspace,
+                      const float* A, const qlora_dx_epilogue* epilogue, void* dX, void* workspace,
                       size_t workspace_bytes, void* stream);
 /* The same on packed int4 codes (qlora_gemm_dx_int4). */
 int qlora_gemm_dx_act_int4(const qlora_layer_desc* d, int M, const void* dY, const uint8_t* Wp, const float* sw,
-                           const float* A, const qlora_dx_epilogue* epilogue, void* dX, const void* workspace,
+                           const float* A, const qlora_dx_epilogue* epilogue, void* dX, void* workspace,
                            size_t workspace_bytes, void* stream);
 
 /* Scales of a rows x cols checkpoint: rows * ceil(cols / 32) (0 for a
  * negative rows or cols < 1). */
 size_t qlora_ckpt_scales(int rows, int cols);
 
-/* Bytes of workspace of qlora_backward_ckpt and qlora_lora_grad_x_ckpt: what
- * qlora_workspace_bytes gives, at the same place, and the X pass's digits of
- * sx G.  0 for an invalid descriptor or M > 1047552. */
+/* Bytes of workspace of qlora_backward_ckpt: what qlora_workspace_bytes gives,
+ * at the same place, then the X pass's digits of sx G and, for large bf16
+ * layers on the current device, the de-quantized kernel (2 K N bytes; layers
+ * whose calls run in turn can share one workspace of the largest size).  0 for
+ * an invalid descriptor or M > 1047552. */
 size_t qlora_ckpt_workspace_bytes(const qlora_layer_desc* d, int M);
 
 /* a5 from the kept codes: dA = c * (Xq sx)^T G [K,r], G from the workspace
- * that a3 filled; overwrites the workspace behind qlora_workspace_bytes.  The
- * sum over the rows runs in integers (sx G as a 31-bit fixed-point value per
+ * that a3 filled; overwrites the workspace behind qlora_workspace_bytes (of
+ * qlora_ckpt_workspace_bytes in all, or at least the digits: 256 + 512
+ * ceil4(r) ceil(M / 128) bytes rounded up to 256).  The sum over the rows runs in integers (sx G as a 31-bit fixed-point value per
  * column of G): dA does not depend on how it is split.  A column of G that
  * holds an infinity or a NaN gives NaN in that column of dA.  At most 1047552
  * rows (QLORA_EUNSUPPORTED). */

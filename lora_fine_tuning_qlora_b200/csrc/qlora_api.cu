@@ -318,7 +318,7 @@ int qlora_quantize_input(const qlora_layer_desc* d, int M, const void* X, const 
 }
 
 // The checks of a forward epilogue and its part of the launch arguments.
-static int forward_epilogue(const qlora_layer_desc* d, const qlora_fwd_epilogue* x, const void* Y, FwdEpilogue& ep) {
+static int forward_epilogue(const qlora_fwd_epilogue* x, const void* Y, FwdEpilogue& ep) {
     if (!x) return QLORA_OK;
     QL_REQUIRE(x->act >= QLORA_ACT_NONE && x->act <= QLORA_ACT_SILU, QLORA_EINVAL, "unknown activation");
     QL_REQUIRE((x->zq == nullptr) == (x->zs == nullptr), QLORA_EINVAL,
@@ -326,8 +326,7 @@ static int forward_epilogue(const qlora_layer_desc* d, const qlora_fwd_epilogue*
     QL_REQUIRE(!x->residual || aligned(x->residual, 16), QLORA_EALIGN, "residual must be 16-byte aligned");
     QL_REQUIRE(!x->zq || (aligned(x->zq, 16) && aligned(x->zs, 4)), QLORA_EALIGN,
                "zq must be 16-byte aligned, zs 4-byte aligned");
-    QL_REQUIRE(static_cast<const void*>(x->zq) != Y || !x->zq, QLORA_EINVAL, "zq must not alias Y");
-    (void)d;
+    QL_REQUIRE(!x->zq || static_cast<const void*>(x->zq) != Y, QLORA_EINVAL, "zq must not alias Y");
     ep.ex = x->act != QLORA_ACT_NONE || x->residual || x->zq;
     ep.act = static_cast<int>(x->act);
     ep.res = x->residual;
@@ -351,7 +350,7 @@ static int gemm_forward_impl(const qlora_layer_desc* d, int M, const int8_t* Xq,
                    (!bias || aligned(bias, 4)) && (!acc || aligned(acc, 4)),
                QLORA_EALIGN, "fp32/int32 vectors must be 4-byte aligned");
     FwdEpilogue ep;
-    rc = forward_epilogue(d, x, Y, ep);
+    rc = forward_epilogue(x, Y, ep);
     if (rc != QLORA_OK) return rc;
     if (M == 0) return QLORA_OK;
     int* status = status_ptr();
@@ -411,7 +410,7 @@ int qlora_forward_act(const qlora_layer_desc* d, int M, const void* X, const int
                    (!bias || aligned(bias, 4)),
                QLORA_EALIGN, "fp32 vectors must be 4-byte aligned");
     FwdEpilogue ep;
-    rc = forward_epilogue(d, epilogue, Y, ep);
+    rc = forward_epilogue(epilogue, Y, ep);
     if (rc != QLORA_OK) return rc;
     if (M == 0) return QLORA_OK;
     int* status = status_ptr();
@@ -572,6 +571,7 @@ static int gemm_dx_impl(const qlora_layer_desc* d, int M, const void* dY, const 
     const size_t dense = x ? dx_dense_bytes(act_of(d), M, d->N, d->K, d->r) : 0;
     const size_t dense_at = ckpt_dense_offset(d, M);
     if (dense && workspace_bytes >= dense_at + dense) {
+        // (the calls that pass an epilogue take a writable workspace)
         uint8_t* Wd = const_cast<uint8_t*>(static_cast<const uint8_t*>(workspace)) + dense_at;
         rc = cuda_status(launch_dequantize(Wq, sw, d->N, d->K, w4, Wd, static_cast<cudaStream_t>(stream)),
                          "de-quantize launch");
@@ -598,14 +598,14 @@ int qlora_gemm_dx_relu(const qlora_layer_desc* d, int M, const void* dY, const i
 }
 
 int qlora_gemm_dx_act(const qlora_layer_desc* d, int M, const void* dY, const int8_t* Wq, const float* sw,
-                      const float* A, const qlora_dx_epilogue* epilogue, void* dX, const void* workspace,
+                      const float* A, const qlora_dx_epilogue* epilogue, void* dX, void* workspace,
                       size_t workspace_bytes, void* stream) {
     if (!epilogue) return fail(QLORA_EINVAL, "NULL pointer argument");
     return gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, epilogue);
 }
 
 int qlora_gemm_dx_act_int4(const qlora_layer_desc* d, int M, const void* dY, const uint8_t* Wp, const float* sw,
-                           const float* A, const qlora_dx_epilogue* epilogue, void* dX, const void* workspace,
+                           const float* A, const qlora_dx_epilogue* epilogue, void* dX, void* workspace,
                            size_t workspace_bytes, void* stream) {
     if (!epilogue) return fail(QLORA_EINVAL, "NULL pointer argument");
     return gemm_dx_impl(d, M, dY, reinterpret_cast<const int8_t*>(Wp), sw, A, nullptr, dX, workspace, workspace_bytes,

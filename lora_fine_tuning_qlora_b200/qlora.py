@@ -648,17 +648,58 @@ def act_fn(name: str) -> int:
     return ACTIVATIONS[name]
 
 
-@dataclass
 class Checkpoint:
     """What a layer's forward keeps for its backward: the input as row codes
-    (Xq, sx), xA = X . A and, where it was asked for, the pre-activation Z in 8
-    bits (zq [M, N], zs [ceil(N / 32), M])."""
+    (Xq [M, K], sx [M]), xA [M, r] = X . A and, where it was asked for, the
+    pre-activation Z in 8 bits (zq [M, N], zs [ceil(N / 32), M]).
 
-    Xq: torch.Tensor
-    sx: torch.Tensor
-    xA: torch.Tensor
-    zq: Optional[torch.Tensor] = None
-    zs: Optional[torch.Tensor] = None
+    ``Checkpoint(Xq, sx, xA, zq, zs)`` holds given tensors;
+    ``Checkpoint.allocate(M, K, r, device)`` makes one allocation for Xq, sx
+    and xA, whose tensors are views made when they are asked for."""
+
+    def __init__(self, Xq: Optional[torch.Tensor] = None, sx: Optional[torch.Tensor] = None,
+                 xA: Optional[torch.Tensor] = None, zq: Optional[torch.Tensor] = None,
+                 zs: Optional[torch.Tensor] = None):
+        self._Xq, self._sx, self._xA = Xq, sx, xA
+        self.zq, self.zs = zq, zs
+        self._block = None  # (fp32 buffer, M, K, r): xA, then sx, then Xq from a 16-byte boundary
+
+    @classmethod
+    def allocate(cls, M: int, K: int, r: int, device=None) -> "Checkpoint":
+        self = cls()
+        head = (M * (r + 1) + 3) // 4 * 4
+        self._block = (torch.empty(head + (M * K + 3) // 4, dtype=torch.float32, device=device or "cuda"), M, K, r)
+        return self
+
+    @property
+    def Xq(self) -> torch.Tensor:
+        if self._Xq is None:
+            buf, M, K, r = self._block
+            self._Xq = buf.view(torch.int8).as_strided((M, K), (K, 1), (M * (r + 1) + 3) // 4 * 16)
+        return self._Xq
+
+    @property
+    def sx(self) -> torch.Tensor:
+        if self._sx is None:
+            buf, M, _, r = self._block
+            self._sx = buf.as_strided((M,), (1,), M * r)
+        return self._sx
+
+    @property
+    def xA(self) -> torch.Tensor:
+        if self._xA is None:
+            buf, M, _, r = self._block
+            self._xA = buf.as_strided((M, r), (r, 1), 0)
+        return self._xA
+
+    def _addresses(self, M: int, K: int, r: int, device):
+        """Checked addresses of Xq, sx and xA for a layer of these sizes."""
+        if self._block is not None and self._block[1:] == (M, K, r) and self._block[0].device == device:
+            base = self._block[0].data_ptr()
+            return base + (M * (r + 1) + 3) // 4 * 16, base + 4 * M * r, base
+        return (_expect(self.Xq, "Xq", (M, K), torch.int8, device),
+                _expect(self.sx, "sx", (M,), torch.float32, device),
+                _expect(self.xA, "xA", (M, r), torch.float32, device))
 
     @property
     def z(self):
@@ -704,9 +745,13 @@ def ckpt_buffers(M: int, N: int, device=None):
             torch.empty((-(-N // CKPT_BLOCK), M), dtype=torch.float32, device=dev))
 
 
+def qlora_ckpt_workspace_bytes(d: LayerDesc, M: int) -> int:
+    return int(_lib.qlora_ckpt_workspace_bytes(ctypes.byref(d), int(M)))
+
+
 def ckpt_workspace(d: LayerDesc, M: int, device=None) -> torch.Tensor:
     """A uint8 device buffer big enough for backward_ckpt at M tokens."""
-    n = int(_lib.qlora_ckpt_workspace_bytes(ctypes.byref(d), int(M)))
+    n = qlora_ckpt_workspace_bytes(d, M)
     if n == 0:
         raise QLoraError(-1, "invalid layer descriptor or more than 1047552 tokens")
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
@@ -736,19 +781,17 @@ def forward_act(layer: Layer, X: torch.Tensor, act: str = "none", residual: Opti
         if Y is None:
             Y = torch.empty((M, N), dtype=layer.act, device=dev)
         if keep is None:
-            zq, zs = ckpt_buffers(M, N, dev) if save_z else (None, None)
-            keep = Checkpoint(torch.empty((M, K), dtype=torch.int8, device=dev),
-                              torch.empty((M,), dtype=torch.float32, device=dev),
-                              torch.empty((M, r), dtype=torch.float32, device=dev), zq, zs)
+            keep = Checkpoint.allocate(M, K, r, dev)
+            if save_z:
+                keep.zq, keep.zs = ckpt_buffers(M, N, dev)
     if save_z and keep.zq is None:
         raise ValueError("save_z needs zq and zs in keep")
-    f32 = torch.float32
-    y, xq = _expect(Y, "Y", (M, N), layer.act, dev), _expect(keep.Xq, "Xq", (M, K), torch.int8, dev)
-    sx, xa = _expect(keep.sx, "sx", (M,), f32, dev), _expect(keep.xA, "xA", (M, r), f32, dev)
+    y = _expect(Y, "Y", (M, N), layer.act, dev)
+    xq, sx, xa = keep._addresses(M, K, r, dev)
     ep = FwdEpilogue(fn, _expect(residual, "residual", (M, N), layer.act, dev), None, None)
     if save_z:
         ep.zq = _expect(keep.zq, "zq", (M, N), torch.int8, dev)
-        ep.zs = _expect(keep.zs, "zs", (-(-N // CKPT_BLOCK), M), f32, dev)
+        ep.zs = _expect(keep.zs, "zs", (-(-N // CKPT_BLOCK), M), torch.float32, dev)
     if M > 0:
         _check(_lib.qlora_forward_act(layer.desc(), M, x, wq, sw, bias, a, b, ep, y, xq, sx, xa, s))
     return Y, keep
@@ -767,21 +810,21 @@ def _dx_epilogue(act: str, z, add, M: int, K: int, dtype, dev) -> DxEpilogue:
 
 def backward_ckpt(layer: Layer, keep: Checkpoint, dY: torch.Tensor, ws: torch.Tensor, act: str = "none", z=None,
                   add: Optional[torch.Tensor] = None, dX: Optional[torch.Tensor] = None, want_dx: bool = True,
-                  want_dbias: bool = True, stream=None):
+                  want_dbias: bool = True, grads=None, stream=None):
     """The layer's gradients from the checkpoint its forward kept: returns
     (dX or None, dA, dB, dbias or None).
 
     ``act`` and ``z`` (the ``Checkpoint.z`` of the layer below) name the
     activation that produced this layer's input: dX is taken back through it.
     ``add`` is added to dX (the gradient of a skip connection; it may be ``dX``
-    itself).  ``ws``: ``ckpt_workspace``."""
+    itself).  ``ws``: ``ckpt_workspace``.  ``grads`` = (dA, dB, dbias or None)
+    gives the parameter gradients' buffers, else they are allocated."""
     dev, s = _on_device(dY, "dY", stream)
     M, (N, K), r = dY.shape[0], layer.Wq.shape, layer.A.shape[1]
     f32 = torch.float32
     dy = _expect(dY, "dY", (M, N), layer.act, dev)
     wq, sw, _, a, b = _check_layer_tensors(layer, dev)
-    xq, sx = _expect(keep.Xq, "Xq", (M, K), torch.int8, dev), _expect(keep.sx, "sx", (M,), f32, dev)
-    xa = _expect(keep.xA, "xA", (M, r), f32, dev)
+    xq, sx, xa = keep._addresses(M, K, r, dev)
     ep = _dx_epilogue(act, z, add, M, K, layer.act, dev)
     w = _expect(ws, "ws", ws.shape, torch.uint8, dev)
     with _allocating_on(stream):
@@ -789,17 +832,21 @@ def backward_ckpt(layer: Layer, keep: Checkpoint, dY: torch.Tensor, ws: torch.Te
             dX = None
         elif dX is None:
             dX = torch.empty((M, K), dtype=layer.act, device=dev)
-        dA = torch.empty((K, r), dtype=f32, device=dev)
-        dB = torch.empty((r, N), dtype=f32, device=dev)
-        dbias = torch.empty((N,), dtype=f32, device=dev) if want_dbias else None
+        if grads is not None:
+            dA, dB, dbias = grads
+        else:
+            dA = torch.empty((K, r), dtype=f32, device=dev)
+            dB = torch.empty((r, N), dtype=f32, device=dev)
+            dbias = torch.empty((N,), dtype=f32, device=dev) if want_dbias else None
+        da, db = _expect(dA, "dA", (K, r), f32, dev), _expect(dB, "dB", (r, N), f32, dev)
+        dbi = _expect(dbias, "dbias", (N,), f32, dev)
         if M == 0:
             for g in (dA, dB, dbias):
                 if g is not None:
                     g.zero_()
             return dX, dA, dB, dbias
     _check(_lib.qlora_backward_ckpt(layer.desc(), M, xq, sx, dy, wq, sw, a, b, xa, ep,
-                                    _expect(dX, "dX", (M, K), layer.act, dev), dA.data_ptr(), dB.data_ptr(),
-                                    dbias.data_ptr() if want_dbias else None, w, ws.numel(), s))
+                                    _expect(dX, "dX", (M, K), layer.act, dev), da, db, dbi, w, ws.numel(), s))
     return dX, dA, dB, dbias
 
 

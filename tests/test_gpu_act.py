@@ -135,3 +135,437 @@ def test_checkpoint_bits(M, N, dt):
         assert torch.equal(back, (q.float() * s.t().repeat_interleave(32, dim=1)[:, :N]).to(out))
     rowq, sx = ref.row_codes(T)
     assert torch.equal(qlora.ckpt_load(rowq, sx, dt), (rowq.float() * sx[:, None]).to(dt))
+
+
+# ------------------------------------------------------------------ beyond shapes
+def _pack_int4(codes):
+    lo, hi = codes[:, 0::2].to(torch.int16) & 0xF, codes[:, 1::2].to(torch.int16) & 0xF
+    return (lo | (hi << 4)).to(torch.uint8).contiguous()
+
+
+@pytest.mark.parametrize("M,K,N,r,dt", [(5, 256, 160, 4, BF16), (200, 288, 161, 8, BF16), (150, 96, 72, 4, F32),
+                                        (2100, 256, 2568, 4, BF16), (2100, 256, 2565, 16, BF16)])
+def test_int4_kernels_match_their_int8_codes(M, K, N, r, dt):
+    """Packed int4 codes give what the same codes give as int8: to the last bit
+    on the same kernel form, to half a step where the forms differ."""
+    g = _gen(11)
+    L = make_layer(K, N, r, dt, g)
+    L.Wq = torch.randint(-7, 8, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    L.sw = L.sw * 16
+    Wp = _pack_int4(L.Wq)
+    X = torch.randn(M, K, generator=g, device="cuda").to(dt)
+    R = torch.randn(M, N, generator=g, device="cuda").to(dt)
+    d = L.desc()
+    Y, keep = qlora.forward_act(L, X, act="gelu", residual=R, save_z=True)
+    Y4, z4 = torch.empty_like(Y), qlora.ckpt_buffers(M, N)
+    qlora.qlora_gemm_forward_act(d, M, keep.Xq, keep.sx, Wp, L.sw, L.bias, keep.xA, L.B, Y4, "gelu", R, z4)
+    y, z, y_err, z_err, *_ = ref.forward(X, L.Wq, L.sw, L.bias, L.A, L.B, L.alpha / r, "gelu", R)
+    ref.check(Y4, y, y_err, "Y int4")
+    step = z4[1].double().t().repeat_interleave(32, dim=1)[:, :N]
+    ref.check(ref.block_values(*z4), z, (0.5 + 128 * ref.U) * step + z_err, "z int4")
+    if K % 32 == 0:
+        dY = (torch.randn(M, N, generator=g, device="cuda") * 0.3).to(dt)
+        zk = ref.block_codes(torch.randn(M, K, generator=g, device="cuda"))
+        ws = qlora.ckpt_workspace(d, M)
+        small = torch.empty(qlora.qlora_workspace_bytes(d, M), dtype=torch.uint8, device="cuda")
+        dB, db = torch.empty(r, N, device="cuda"), torch.empty(N, device="cuda")
+        add = torch.randn(M, K, generator=g, device="cuda").to(dt)
+        want = ref.backward(dY, keep.Xq, keep.sx, L.Wq, L.sw, L.A, L.B, keep.xA, L.alpha / r, "gelu", zk, add)["dX"]
+        # G of the 16-bit dY pass: 2^-16 of the factor's magnitude sums more
+        G_mag = dY.double().abs() @ L.B.double().abs().t()
+        sl = ref.slope("gelu", ref.block_values(*zk)).abs()
+        extra = 1.01 * L.alpha / r * 2.0 ** -16 * (G_mag @ L.A.double().abs().t()) * sl
+        for w in (ws, small):
+            qlora.qlora_lora_grad_dy(d, M, dY, L.B, keep.xA, dB, db, w)
+            for W in (L.Wq, Wp):
+                dX = torch.full((M, K), float("nan"), dtype=dt, device="cuda")
+                qlora.qlora_gemm_dx_act(d, M, dY, W, L.sw, L.A, dX, w, "gelu", zk, add)
+                ref.check(dX, want[0], want[1] + extra, "dX")
+
+
+@pytest.mark.parametrize("M,K,N,dt", [(9, 64, 72, BF16), (200, 64, 77, F32), (2048, 64, 2560, BF16)])
+def test_residual_and_add_in_place(M, K, N, dt):
+    L, X, Y, keep = run_forward(M, K, N, 4, dt, "silu", False, False, seed=2)
+    R = torch.randn(M, N, device="cuda").to(dt)
+    Y1, _ = qlora.forward_act(L, X, act="silu", residual=R)
+    R2 = R.clone()
+    Y2, _ = qlora.forward_act(L, X, act="silu", residual=R2, Y=R2)
+    assert Y2 is R2 and torch.equal(Y1, Y2)
+    dY = torch.randn(M, N, device="cuda").to(dt)
+    z = ref.block_codes(torch.randn(M, K, device="cuda"))
+    ws = qlora.ckpt_workspace(L.desc(), M)
+    add = torch.randn(M, K, device="cuda").to(dt)
+    want = qlora.backward_ckpt(L, keep, dY, ws, act="silu", z=z, add=add)
+    buf = add.clone()
+    got = qlora.backward_ckpt(L, keep, dY, ws, act="silu", z=z, add=buf, dX=buf)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_nothing_outside_the_outputs_is_written():
+    M, K, N, r = 333, 272, 200, 4
+    g = _gen(4)
+    L = make_layer(K, N, r, BF16, g)
+    X = torch.randn(M, K, generator=g, device="cuda").to(BF16)
+
+    def guarded(shape, dtype):
+        n = math.prod(shape)
+        whole = torch.full((n + 256,), 77, dtype=dtype, device="cuda")
+        return whole, whole[128:128 + n].view(shape)
+
+    wy, Y = guarded((M, N), BF16)
+    wz, zq = guarded((M, N), torch.int8)
+    ws_, zs = guarded((7, M), F32)
+    keep = qlora.Checkpoint.allocate(M, K, r)
+    keep.zq, keep.zs = zq, zs
+    qlora.forward_act(L, X, act="gelu", save_z=True, keep=keep, Y=Y)
+    wx, dX = guarded((M, K), BF16)
+    wa, dA = guarded((K, r), F32)
+    wb, dB = guarded((r, N), F32)
+    wc, db = guarded((N,), F32)
+    z = ref.block_codes(torch.randn(M, K, generator=g, device="cuda"))
+    qlora.backward_ckpt(L, keep, Y, qlora.ckpt_workspace(L.desc(), M), act="gelu", z=z, dX=dX, grads=(dA, dB, db))
+    for w in (wy, wz, ws_, wx, wa, wb, wc):
+        assert bool((w[:128] == 77).all()) and bool((w[-128:] == 77).all())
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,N", [(40, 64), (37, 1030), (5, 72)])
+def test_checkpoint_of_extreme_values(M, N, dt):
+    T = torch.randn(M, N, device="cuda")
+    T[0, 0], T[1, 3], T[2, 5] = math.inf, -math.inf, math.nan
+    T[3] = 0
+    T[4] = 2.0 ** -101
+    if M > 6:
+        T[5], T[6] = 3e38, 2.0 ** -99
+    T = T.to(dt)
+    q, s = qlora.ckpt_save(T)
+    rq, rs = ref.block_codes(T)
+    assert torch.equal(q, rq) and torch.equal(s.view(torch.int32), rs.view(torch.int32).where(~rs.isnan(), s.view(torch.int32)))
+    assert torch.equal(s.isnan(), rs.isnan()) and int(s.isnan().sum()) == 3
+    back = qlora.ckpt_load(q, s, dt)
+    assert int(back.isnan().sum()) == 3 * min(32, N) and back[3].abs().max() == 0 and back[4].abs().max() == 0
+
+
+def test_activations_of_extreme_values():
+    """Z = bias where the kernel is zero: saturated arguments, infinities and
+    NaN come out as the formulas say, on every forward form."""
+    b = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 30.0, -30.0, 200.0, -200.0, 1e20, -1e20, 3e38, -3e38, math.inf, math.nan,
+                      5.0, -5.0], device="cuda")
+    for M, K, N in ((3, 32, 16), (200, 32, 16), (2048, 32, 2560)):
+        bias = b.repeat(N // 16)
+        for dt in (BF16, F32):
+            L = qlora.Layer(torch.zeros(N, K, dtype=torch.int8, device="cuda"), torch.ones(N, device="cuda"), bias,
+                            torch.zeros(K, 2, device="cuda"), torch.zeros(2, N, device="cuda"), 2.0, dt)
+            X = torch.ones(M, K, device="cuda", dtype=dt)
+            for name in ("relu", "gelu", "gelu_tanh", "silu"):
+                Y, keep = qlora.forward_act(L, X, act=name, save_z=True)
+                z = b.double()
+                want = ref.act(name, z.clamp(-1e6, 1e6))
+                want[8:14] = torch.tensor([1e20, 0, 3e38, 0, math.inf, math.nan], dtype=torch.float64)
+                if name == "gelu":
+                    want[9] = want[11] = 0
+                want = want.to(F32).to(dt).double()
+                got = Y.double()[:, :16]
+                # (fp32 outputs split the bias into two parts, so an infinity may come out as NaN)
+                assert bool(got[:, 13].isnan().all()) and not bool(got[:, 12].isfinite().any())
+                ok = [i for i in range(16) if i not in (12, 13)]
+                err = 2 * ref.half_step(dt) * want.abs() + 1e-6 + 4e-7 * z.abs().clamp_max(300)
+                assert bool(((got - want).abs() <= err)[:, ok].all()), (name, dt, M, got[0], want)
+                # the block with the infinity and the NaN reads back as NaN
+                assert bool(keep.zs[0].isnan().all()) and int(keep.zq[:, :16].abs().sum()) == 0
+
+
+@pytest.mark.parametrize("name", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M", [32, 128])
+def test_slope_is_the_difference_quotient_of_the_forward(name, M):
+    """dX / sum(dY w) on one side, (act(z + h) - act(z - h)) / 2h on the other,
+    both from the kernels in fp32."""
+    K = N = 64
+    z = torch.linspace(-6, 6, M * K, device="cuda").view(M, K)
+    zc = ref.block_codes(z)
+    zv = ref.block_values(*zc).float()
+    eye = torch.eye(K, dtype=torch.int8, device="cuda")
+    L = qlora.Layer(eye, torch.ones(K, device="cuda"), None, torch.zeros(K, 1, device="cuda"),
+                    torch.zeros(1, K, device="cuda"), 1.0, F32)
+    keep = qlora.Checkpoint(torch.zeros(M, K, dtype=torch.int8, device="cuda"), torch.zeros(M, device="cuda"),
+                            torch.zeros(M, 1, device="cuda"))
+    dX, *_ = qlora.backward_ckpt(L, keep, torch.ones(M, K, device="cuda"), qlora.ckpt_workspace(L.desc(), M), act=name,
+                                 z=zc)
+    h = 2.0 ** -6
+    zero = torch.zeros(K, K, dtype=torch.int8, device="cuda")
+
+    def act(v):  # act of a row of values: the bias of a zero kernel
+        out = torch.empty(M, K, device="cuda")
+        for m in range(M):
+            Z = qlora.Layer(zero, torch.ones(K, device="cuda"), v[m].contiguous(), L.A, L.B, 1.0, F32)
+            out[m] = qlora.forward_act(Z, torch.ones(1, K, device="cuda"), act=name)[0][0]
+        return out
+
+    num = (act(zv + h) - act(zv - h)) / (2 * h)
+    # h^2 / 6 times a third derivative below 3; both values to 4e-7 |z| + 2e-7 over 2 h
+    tol = h * h / 2 + (4e-7 * zv.abs() + 4e-7) / h
+    assert bool(((num - dX).abs() <= tol).all()), float(((num - dX).abs() - tol).max())
+
+
+@pytest.mark.parametrize("M,K,r", [(1, 16, 1), (130, 48, 3), (1000, 272, 8), (4096, 144, 33), (300, 80, 64)])
+def test_grad_a_does_not_depend_on_the_split(M, K, r):
+    """The sum over the rows runs in integers: the same bits for every split."""
+    g = _gen(M)
+    L = make_layer(K, 40, r, BF16, g)
+    X = torch.randn(M, K, generator=g, device="cuda")
+    q, sx = ref.row_codes(X)
+    dY = torch.randn(M, 40, generator=g, device="cuda").to(BF16)
+    d, ws = L.desc(), qlora.ckpt_workspace(L.desc(), M)
+    xA = X @ L.A
+    qlora.qlora_lora_grad_dy(d, M, dY, L.B, xA, torch.empty(r, 40, device="cuda"), torch.empty(40, device="cuda"), ws)
+    out = []
+    for rows in (0, 128, 256, 1024, 1 << 24):
+        prev = qlora.qlora_set_rank_pass_rows(rows)
+        try:
+            dA = torch.full((K, r), float("nan"), device="cuda")
+            qlora.qlora_lora_grad_x_ckpt(d, M, q, sx, dA, ws)
+        finally:
+            qlora.qlora_set_rank_pass_rows(prev)
+        out.append(dA)
+    assert all(torch.equal(out[0], o) for o in out)
+
+
+def test_grad_a_at_the_largest_sums():
+    """130944 rows in one CTA, every product at its largest: int32 holds it."""
+    M, K, r = 1023 * 128 + 5, 16, 4
+    L = make_layer(K, 8, r, BF16, _gen(0))
+    L.B = torch.ones(r, 8, device="cuda")
+    q = torch.full((M, K), 127, dtype=torch.int8, device="cuda")
+    q[:, 1::2] = -127
+    sx = torch.full((M,), 0.5, device="cuda")
+    dY = torch.full((M, 8), 1.0, device="cuda", dtype=BF16)
+    ws = qlora.ckpt_workspace(L.desc(), M)
+    prev = qlora.qlora_set_rank_pass_rows(1 << 24)
+    try:
+        _, dA, dB, db = qlora.backward_ckpt(L, qlora.Checkpoint(q, sx, torch.ones(M, r, device="cuda")), dY, ws,
+                                            want_dx=False)
+    finally:
+        qlora.qlora_set_rank_pass_rows(prev)
+    want = 2.0 * 127 * 0.5 * 8 * M  # c = 2
+    assert bool((dA[0::2] == want).all()) and bool((dA[1::2] == -want).all())
+    assert bool(((db - M).abs() <= (M + 10) * ref.U * M).all())
+
+
+def test_non_finite_gradients_show():
+    """A token with an infinite gradient: NaN in dA, and other tokens' dX intact."""
+    M, K, N, r = 200, 64, 48, 4
+    L = make_layer(K, N, r, BF16, _gen(1))
+    q, sx = ref.row_codes(torch.randn(M, K, device="cuda"))
+    keep = qlora.Checkpoint(q, sx, torch.randn(M, r, device="cuda"))
+    ws = qlora.ckpt_workspace(L.desc(), M)
+    dY = torch.randn(M, N, device="cuda").to(BF16)
+    clean, *_ = qlora.backward_ckpt(L, keep, dY, ws)
+    dY[77, 5] = math.inf
+    dX, dA, dB, _ = qlora.backward_ckpt(L, keep, dY, ws)
+    assert bool(dA.isnan().all()) and not bool(dB.isfinite().all())
+    rest = [m for m in range(M) if m != 77]
+    assert torch.equal(dX[rest], clean[rest])
+
+
+def test_empty_batch():
+    L = make_layer(32, 24, 4, BF16, _gen(1))
+    Y, keep = qlora.forward_act(L, torch.empty(0, 32, dtype=BF16, device="cuda"), act="gelu", save_z=True)
+    assert Y.shape == (0, 24) and keep.zq.shape == (0, 24)
+    dX, dA, dB, db = qlora.backward_ckpt(L, keep, Y, qlora.ckpt_workspace(L.desc(), 0))
+    assert dX.shape == (0, 32) and not bool(dA.any()) and not bool(dB.any()) and not bool(db.any())
+    q, s = qlora.ckpt_save(torch.empty(0, 40, device="cuda"))
+    assert qlora.ckpt_load(q, s).shape == (0, 40)
+
+
+def test_refusals_of_the_binding():
+    L = make_layer(32, 24, 4, BF16, _gen(1))
+    X = torch.zeros(8, 32, dtype=BF16, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        qlora.forward_act(L, torch.zeros(32, 8, dtype=BF16, device="cuda").t())
+    with pytest.raises(ValueError, match="X must be"):
+        qlora.forward_act(L, X.float())
+    with pytest.raises(ValueError, match="residual must be"):
+        qlora.forward_act(L, X, residual=X)
+    with pytest.raises(ValueError, match="needs z"):
+        Y, keep = qlora.forward_act(L, X)
+        qlora.backward_ckpt(L, keep, Y, qlora.ckpt_workspace(L.desc(), 8), act="gelu")
+    with pytest.raises(ValueError, match="zs must be"):
+        qlora.backward_ckpt(L, keep, Y, qlora.ckpt_workspace(L.desc(), 8), act="gelu",
+                            z=(torch.zeros(8, 32, dtype=torch.int8, device="cuda"), torch.zeros(8, 1, device="cuda")))
+    with pytest.raises(qlora.QLoraError):
+        qlora.backward_ckpt(L, keep, Y, torch.empty(256, dtype=torch.uint8, device="cuda"))
+    odd = torch.zeros(8 * 32 + 4, dtype=BF16, device="cuda")[4:].view(8, 32)  # 8-byte aligned
+    with pytest.raises(qlora.QLoraError):
+        qlora.forward_act(L, odd)
+    with pytest.raises(ValueError, match="scales must be"):
+        qlora.ckpt_load(torch.zeros(8, 64, dtype=torch.int8, device="cuda"), torch.zeros(3, 8, device="cuda"))
+
+
+def test_streams_and_two_calls_at_once():
+    """Calls on two side streams with workspaces of their own, and outputs
+    allocated on the stream that writes them."""
+    M, K, N, r = 700, 272, 320, 4
+    L = make_layer(K, N, r, BF16, _gen(5))
+    X = torch.randn(M, K, device="cuda").to(BF16)
+    dY = torch.randn(M, N, device="cuda").to(BF16)
+    Y0, keep0 = qlora.forward_act(L, X, act="silu", save_z=True)
+    g0 = qlora.backward_ckpt(L, keep0, dY, qlora.ckpt_workspace(L.desc(), M))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    work = [qlora.ckpt_workspace(L.desc(), M) for _ in streams]
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(4):
+        for s, w in zip(streams, work):
+            Y, keep = qlora.forward_act(L, X, act="silu", save_z=True, stream=s)
+            out.append((Y, keep, qlora.backward_ckpt(L, keep, dY, w, stream=s)))
+    torch.cuda.synchronize()
+    for Y, keep, gr in out:
+        assert torch.equal(Y, Y0) and torch.equal(keep.zq, keep0.zq) and torch.equal(keep.zs, keep0.zs)
+        assert all(torch.equal(a, b) for a, b in zip(gr, g0))
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements on every side that grows with the tokens."""
+    M, K, N, r = 530000, 16, 4096, 4
+    L = make_layer(K, N, r, BF16, _gen(6))
+    X = torch.randn(M, K, device="cuda").to(BF16)
+    Y, keep = qlora.forward_act(L, X, act="relu", save_z=True)
+    rows = torch.cat([torch.arange(0, 3), torch.arange(262100, 262180), torch.arange(524280, 524300),
+                      torch.arange(M - 40, M)]).cuda()
+    y, z, y_err, z_err, *_ = ref.forward(X[rows], L.Wq, L.sw, L.bias, L.A, L.B, L.alpha / r, "relu", None)
+    ref.check(Y[rows], y, y_err, "Y")
+    zs = keep.zs[:, rows]
+    step = zs.double().t().repeat_interleave(32, dim=1)
+    ref.check(keep.zq[rows].double() * step, z, (0.5 + 128 * ref.U) * step + z_err, "z")
+    back = qlora.ckpt_load(keep.zq, keep.zs, BF16)
+    assert torch.equal(back[rows], (keep.zq[rows].float() * zs.t().repeat_interleave(32, dim=1)).to(BF16))
+    del back, keep
+    q, s = qlora.ckpt_save(Y)
+    rq, rs = ref.block_codes(Y[rows])
+    assert torch.equal(q[rows], rq) and torch.equal(s[:, rows], rs)
+    del q, s
+    # the backward of the layer above: N wide on the input side
+    U_ = make_layer(N, 16, r, BF16, _gen(7))
+    Yc, sx = ref.row_codes(X.float())
+    dY = torch.randn(M, 16, device="cuda").to(BF16)
+    z = (torch.randint(-127, 128, (M, N), dtype=torch.int8, device="cuda"),
+         torch.rand(N // 32, M, device="cuda") * 0.03)
+    dX = torch.empty(M, N, dtype=BF16, device="cuda")
+    ws = qlora.ckpt_workspace(U_.desc(), M)
+    qlora.qlora_lora_grad_dy(U_.desc(), M, dY, U_.B, torch.zeros(M, r, device="cuda"), torch.empty(r, 16, device="cuda"),
+                             torch.empty(16, device="cuda"), ws)
+    qlora.qlora_gemm_dx_act(U_.desc(), M, dY, U_.Wq, U_.sw, U_.A, dX, ws, "silu", z, None)
+    zr = (z[0][rows], z[1][:, rows].contiguous())
+    want = ref.backward(dY[rows], z[0][rows], sx[rows], U_.Wq, U_.sw, U_.A, U_.B, torch.zeros(len(rows), r).cuda(),
+                        U_.alpha / r, "silu", zr, None)["dX"]
+    G_mag = dY[rows].double().abs() @ U_.B.double().abs().t()
+    extra = 1.2 * U_.alpha / r * 2.0 ** -16 * (G_mag @ U_.A.double().abs().t())
+    ref.check(dX[rows], want[0], want[1] + extra, "dX")
+    # dA over more than 2^31 codes, against the same sum in pieces of 64 bits
+    dA = torch.empty(N, r, device="cuda")
+    qlora.qlora_lora_grad_x_ckpt(U_.desc(), M, z[0], sx, dA, ws)
+    V = sx.double()[:, None] * (dY.double() @ U_.B.double().t())
+    want, mag = torch.zeros(N, r, dtype=torch.float64, device="cuda"), torch.zeros(N, r, dtype=torch.float64, device="cuda")
+    for m in range(0, M, 32768):
+        c = z[0][m:m + 32768].double()
+        want += c.t() @ V[m:m + 32768]
+        mag += c.abs().t() @ (sx.double()[m:m + 32768, None] * G_abs(dY[m:m + 32768], U_.B))
+    scale = U_.alpha / r
+    # G at 16 bits of B and fp32 sums of 16 terms, V to 31 bits below its column's maximum
+    err = scale * ((2.0 ** -16 + 30 * ref.U) * mag + 127.0 * M * 2.0 ** -29 * V.abs().amax(dim=0))
+    ref.check(dA, scale * want, err, "dA")
+
+
+def G_abs(dY, B):
+    return dY.double().abs() @ B.double().abs().t()
+
+
+# ------------------------------------------------------------------ a run of them together
+def make_block(M, K, N, r, dt, name, skip=True, seed=0):
+    from lora_fine_tuning_qlora_b200.feedforward import FeedForward
+    g = _gen(seed)
+    ff = FeedForward(make_layer(K, N, r, dt, g), make_layer(N, K, r, dt, g), M, act=name, skip=skip)
+    ff.X.copy_(torch.randn(M, K, generator=g, device="cuda").to(dt))
+    ff.dY.copy_((torch.randn(M, K, generator=g, device="cuda") * 0.1).to(dt))
+    return ff
+
+
+def check_block(ff):
+    """Each stage against the reference on the stage's own inputs."""
+    u, d, s = ff.up, ff.down, ff.up.alpha / ff.up.r
+    y, z, y_err, z_err, xa, xa_err, q, sx = ref.forward(ff.X, u.Wq, u.sw, u.bias, u.A, u.B, s, ff.act, None)
+    ref.check(ff.H, y, y_err, "H")
+    assert torch.equal(ff.keep_up.Xq, q) and torch.equal(ff.keep_up.sx, sx)
+    y, _, y_err, *_ = ref.forward(ff.H, d.Wq, d.sw, d.bias, d.A, d.B, d.alpha / d.r, "none", ff.X if ff.skip else None)
+    ref.check(ff.Y, y, y_err, "Y")
+    for L, keep, dy, name, zz, add, dx, grads in (
+            (d, ff.keep_down, ff.dY, ff.act, ff.keep_up.z, None, ff.dZ, ff.grads[1]),
+            (u, ff.keep_up, ff.dZ, "none", None, ff.dY if ff.skip else None, ff.dX, ff.grads[0])):
+        want = ref.backward(dy, keep.Xq, keep.sx, L.Wq, L.sw, L.A, L.B, keep.xA, L.alpha / L.r, name, zz, add)
+        for key, got in zip(("dX", "dA", "dB", "dbias"), (dx,) + grads):
+            ref.check(got, *want[key], key)
+    assert qlora.qlora_device_status() == 0
+
+
+@pytest.mark.parametrize("M,K,N,r,dt,name,skip", [
+    (7, 64, 160, 4, BF16, "gelu_tanh", True), (100, 64, 96, 4, F32, "gelu", True), (640, 272, 528, 8, BF16, "silu", False),
+    (2048, 528, 2576, 4, BF16, "gelu", True)])
+def test_feed_forward_block(M, K, N, r, dt, name, skip):
+    ff = make_block(M, K, N, r, dt, name, skip)
+    ff.step()
+    check_block(ff)
+    assert ff.kept_bytes() < 0.6 * M * (2 * K + 4 * N) * (ff.X.element_size() / 2) + M * 8 * (r + 2)
+
+
+@pytest.mark.parametrize("M,dt", [(48, BF16), (300, F32), (1100, BF16)])
+def test_captured_blocks_replay_on_new_inputs(M, dt):
+    """Two captured blocks (each with its own workspace) replayed in turn and
+    overlapping, on inputs that they were not captured with, give what eager
+    steps give, bit for bit."""
+    blocks = [make_block(M, 64, 160, 4, dt, "silu", seed=s) for s in (1, 2)]
+    for b in blocks:
+        b.capture()
+    for rep in range(3):
+        for i, b in enumerate(blocks):
+            b.X.copy_(torch.randn(M, 64, generator=_gen(10 * rep + i), device="cuda").to(dt))
+            b.dY.copy_(torch.randn(M, 64, generator=_gen(99 + rep + i), device="cuda").to(dt))
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in blocks]
+        for b, s in zip(blocks, streams):
+            with torch.cuda.stream(s):
+                b.replay()
+        torch.cuda.synchronize()
+        for b in blocks:
+            got = [t.clone() for t in (b.Y, b.dX, b.grad_flat, b.keep_up.zq, b.keep_up.zs)]
+            b.step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(got, (b.Y, b.dX, b.grad_flat, b.keep_up.zq, b.keep_up.zs)))
+    check_block(blocks[0])
+
+
+def test_repeated_calls_give_the_same_bits():
+    ff = make_block(1500, 256, 512, 8, BF16, "gelu")
+    ff.step()
+    first = [t.clone() for t in (ff.Y, ff.dX, ff.grad_flat)]
+    for _ in range(3):
+        ff.ws.fill_(0xFF)
+        ff.step()
+        assert all(torch.equal(a, b) for a, b in zip(first, (ff.Y, ff.dX, ff.grad_flat)))
+
+
+def test_old_entry_points_share_no_state_with_the_new():
+    """The composite backward's results do not change when calls of the new
+    kind run between."""
+    M, K, N, r = 600, 272, 320, 4
+    L = make_layer(K, N, r, BF16, _gen(8))
+    X = torch.randn(M, K, device="cuda").to(BF16)
+    ws = qlora.ckpt_workspace(L.desc(), M)
+    Y, xA = qlora.forward(L, X, ws)
+    before = qlora.backward(L, X, Y, xA, ws)
+    Y2, keep = qlora.forward_act(L, X, act="silu", save_z=True)
+    qlora.backward_ckpt(L, keep, Y2, ws)
+    Y3, xA3 = qlora.forward(L, X, ws)
+    after = qlora.backward(L, X, Y3, xA3, ws)
+    assert torch.equal(Y, Y3) and all(torch.equal(a, b) for a, b in zip(before, after))
