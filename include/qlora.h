@@ -524,8 +524,9 @@ int qlora_lora_grad_x_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, c
  * qlora_gemm_dx_act (dX NULL: left out; epilogue NULL: no activation, nothing
  * added) and qlora_lora_grad_x_ckpt.  In bf16 the factors B and xA of the dY
  * pass enter at 24 bits for r <= 32 (16 in qlora_backward and for larger r).
- * Workspace of qlora_ckpt_workspace_bytes; streams, capture and the second
- * stream from 512 tokens as qlora_backward.  Deterministic. */
+ * Workspace of qlora_ckpt_workspace_bytes; streams and capture as
+ * qlora_backward, the second stream from 512 tokens and M K N >= 2^28, also for
+ * the kernel's de-quantization beside the dY pass.  Deterministic. */
 int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx, const void* dY,
                         const int8_t* Wq, const float* sw, const float* A, const float* B, const float* xA,
                         const qlora_dx_epilogue* epilogue, void* dX, float* dA, float* dB, float* dbias,

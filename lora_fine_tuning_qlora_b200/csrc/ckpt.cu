@@ -146,39 +146,57 @@ __global__ void __launch_bounds__(kCkThreads) ckpt_load_kernel(const int8_t* __r
     }
 }
 
-// Any column count: one thread per block and row, element by element.
+// Any column count: a warp takes blocks of 32 columns, a lane each, of kCkRows
+// consecutive rows, element by element.
 template <typename T>
 __global__ void __launch_bounds__(kCkThreads) ckpt_save_any_kernel(const T* __restrict__ X, int rows, int cols, int nb,
                                                                    int8_t* __restrict__ q, float* __restrict__ scales) {
     pdl_trigger();
     pdl_wait();
-    const size_t items = static_cast<size_t>(rows) * nb;
-    for (size_t i = blockIdx.x * static_cast<size_t>(kCkThreads) + threadIdx.x; i < items;
-         i += static_cast<size_t>(gridDim.x) * kCkThreads) {
-        const int b = static_cast<int>(i / rows), row = static_cast<int>(i - static_cast<size_t>(b) * rows);
-        RowPiece<T, kCkptBlock> p;
-        p.load(X, row, true, b * kCkptBlock, cols, false);
-        float v[kCkptBlock];
+    const int lane = threadIdx.x & 31;
+    const size_t total = static_cast<size_t>((rows + kCkRows - 1) / kCkRows) * nb;
+    for (size_t w = blockIdx.x * static_cast<size_t>(kCkThreads / 32) + threadIdx.x / 32; w < total;
+         w += static_cast<size_t>(gridDim.x) * (kCkThreads / 32)) {
+        const int g = static_cast<int>(w / nb), b = static_cast<int>(w - static_cast<size_t>(g) * nb);
+        const int row0 = g * kCkRows, col = b * kCkptBlock + lane;
+        float v[kCkRows];
 #pragma unroll
-        for (int e = 0; e < kCkptBlock; ++e) v[e] = 0.f;
-        p.add_to(v);
-        ckpt_store(v, q, scales, row, rows, b * kCkptBlock, cols);
+        for (int u = 0; u < kCkRows; ++u)
+            v[u] = col < cols && row0 + u < rows ? ActIO<T>::to_f(X[static_cast<size_t>(row0 + u) * cols + col]) : 0.f;
+#pragma unroll
+        for (int u = 0; u < kCkRows; ++u) {
+            float inv, scale;
+            ckpt_scale(__reduce_max_sync(0xffffffffu, abs_bits(v[u])), inv, scale);
+            if (row0 + u >= rows) break;
+            if (col < cols) q[static_cast<size_t>(row0 + u) * cols + col] = static_cast<int8_t>(quant_code(v[u], inv));
+            if (lane == 0) scales[static_cast<size_t>(b) * rows + row0 + u] = scale;
+        }
     }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kCkThreads) ckpt_load_any_kernel(const int8_t* __restrict__ q,
                                                                    const float* __restrict__ scales, int rows, int cols,
-                                                                   int block, T* __restrict__ X) {
+                                                                   int nb, int block, T* __restrict__ X) {
     pdl_trigger();
     pdl_wait();
-    const size_t n = static_cast<size_t>(rows) * cols;
-    for (size_t i = blockIdx.x * static_cast<size_t>(kCkThreads) + threadIdx.x; i < n;
-         i += static_cast<size_t>(gridDim.x) * kCkThreads) {
-        const size_t row = i / cols;
-        const int col = static_cast<int>(i - row * cols);
-        const float s = __ldg(scales + (block ? static_cast<size_t>(col / kCkptBlock) * rows : 0) + row);
-        X[i] = ActIO<T>::from_f(static_cast<float>(q[i]) * s);
+    const int lane = threadIdx.x & 31;
+    const size_t total = static_cast<size_t>((rows + kCkRows - 1) / kCkRows) * nb;
+    for (size_t w = blockIdx.x * static_cast<size_t>(kCkThreads / 32) + threadIdx.x / 32; w < total;
+         w += static_cast<size_t>(gridDim.x) * (kCkThreads / 32)) {
+        const int g = static_cast<int>(w / nb), b = static_cast<int>(w - static_cast<size_t>(g) * nb);
+        const int row0 = g * kCkRows, col = b * kCkptBlock + lane;
+        if (col >= cols) continue;
+        float v[kCkRows];
+#pragma unroll
+        for (int u = 0; u < kCkRows; ++u) {
+            const int row = row0 + u < rows ? row0 + u : rows - 1;
+            v[u] = static_cast<float>(q[static_cast<size_t>(row) * cols + col]) *
+                   __ldg(scales + (block ? static_cast<size_t>(b) * rows : 0) + row);
+        }
+#pragma unroll
+        for (int u = 0; u < kCkRows; ++u)
+            if (row0 + u < rows) X[static_cast<size_t>(row0 + u) * cols + col] = ActIO<T>::from_f(v[u]);
     }
 }
 
@@ -210,8 +228,8 @@ cudaError_t save_t(const T* X, int rows, int cols, int8_t* q, float* scales, cud
                         q, scales);
     }
     const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
-    return launch_k(ckpt_save_any_kernel<T>, ck_grid((static_cast<size_t>(rows) * nb + 31) / 32), dim3(kCkThreads), 0,
-                    s, 1, X, rows, cols, nb, q, scales);
+    return launch_k(ckpt_save_any_kernel<T>, ck_grid(static_cast<size_t>((rows + kCkRows - 1) / kCkRows) * nb),
+                    dim3(kCkThreads), 0, s, 1, X, rows, cols, nb, q, scales);
 }
 
 template <typename T>
@@ -221,8 +239,9 @@ cudaError_t load_t(const int8_t* q, const float* scales, int rows, int cols, int
         return launch_k(ckpt_load_kernel<T>, ck_grid(ck_warps(rows, cols / 8, lanes)), dim3(kCkThreads), 0, s, 1, q,
                         scales, rows, cols, lanes, block, X);
     }
-    return launch_k(ckpt_load_any_kernel<T>, ck_grid((static_cast<size_t>(rows) * cols + 31) / 32), dim3(kCkThreads), 0,
-                    s, 1, q, scales, rows, cols, block, X);
+    const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
+    return launch_k(ckpt_load_any_kernel<T>, ck_grid(static_cast<size_t>((rows + kCkRows - 1) / kCkRows) * nb),
+                    dim3(kCkThreads), 0, s, 1, q, scales, rows, cols, nb, block, X);
 }
 
 }  // namespace

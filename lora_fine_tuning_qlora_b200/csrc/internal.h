@@ -134,7 +134,8 @@ cudaError_t launch_gemm_dx_pair(const void* dY, const int8_t* Wq, const float* s
 // the MMA's N, output channels on its M, the contraction split over a
 // cluster (small_m.cu).  int8 or packed int4 codes (w4) with a scale per
 // row; not the outlier-compensated kernels.
-bool small_m_applies(int M, int out_channels, int r);
+// ex: the EX forms, also taken by up to 256 tokens with few large tiles.
+bool small_m_applies(int M, int out_channels, int r, int contraction = 0, bool ex = false);
 cudaError_t launch_gemm_i8_fwd_small(Act act, const int8_t* Xq, const int8_t* Wq, int M, int N, int K,
                                      const FwdEpilogue& ep, int* status, cudaStream_t s, bool w4);
 cudaError_t launch_gemm_dx_small(const void* dY, const int8_t* Wq, const float* sw, int M, int N, int K,

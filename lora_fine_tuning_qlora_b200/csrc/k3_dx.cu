@@ -11,7 +11,7 @@ cudaError_t launch_gemm_dx(Act act, const void* dY, const int8_t* Wq, const floa
     if (!tc)
         return ep.ex ? launch_gemm_dx_simt_act(act, dY, Wq, sw, M, N, K, ep, s, w4)
                      : launch_gemm_dx_simt(act, dY, Wq, sw, M, N, K, ep, s, mode);
-    if (mode != 2 && !ep.bias && small_m_applies(M, K, ep.r))
+    if (mode != 2 && !ep.bias && small_m_applies(M, K, ep.r, N, ep.ex))
         return launch_gemm_dx_small(dY, Wq, sw, M, N, K, ep, status, s, w4);
     if (gemm_dx_pair_applies(M, N, K, ep.r))
         return launch_gemm_dx_pair(dY, Wq, sw, M, N, K, ep, status, s, w4);

@@ -9,7 +9,9 @@
 // no memory latency (one buffer with the loads between two barriers: 34 us at
 // 64 x 784 x 128 in the backward, 13 CTAs on 8 steps of 16).  Fp32 products
 // and sums; for bf16 activations the kernel is rounded to bf16 first, as on
-// the tensor cores.
+// the tensor cores.  Few tiles share their contraction over a cluster of S CTAs
+// (along x), whose partial tiles the first adds in rank order through
+// distributed shared memory.
 #include "dx_common.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -27,7 +29,7 @@ template <typename T, bool W4, int TM>
 __global__ void __launch_bounds__(kThreads) k3_simt_act_kernel(const T* __restrict__ dY,
                                                                const uint8_t* __restrict__ Wq,
                                                                const float* __restrict__ sw, int M, int N, int K,
-                                                               DxEpilogue ep) {
+                                                               int S, DxEpilogue ep) {
     constexpr int kRows = 16 * TM;
     constexpr int kPerD = kRows * kStep / kThreads;
     __shared__ __align__(16) float sW[2][kStep][kCols];
@@ -38,7 +40,10 @@ __global__ void __launch_bounds__(kThreads) k3_simt_act_kernel(const T* __restri
     pdl_wait();
     const int tid = threadIdx.x;
     const int tx = tid % 16, ty = tid / 16;
-    const int m0 = blockIdx.y * kRows, k0 = blockIdx.x * kCols;
+    const int split = static_cast<int>(blockIdx.x) % S;
+    const int m0 = blockIdx.y * kRows, k0 = static_cast<int>(blockIdx.x) / S * kCols;
+    const int steps = (N + kStep - 1) / kStep;
+    const int nbeg = steps * split / S * kStep, nend = min(N, steps * (split + 1) / S * kStep);
     // a thread's part of a step: kPerD values of dY (consecutive threads along
     // n), eight codes of one contraction row
     const int wn = tid / 8, wk = (tid % 8) * 8;
@@ -50,12 +55,12 @@ __global__ void __launch_bounds__(kThreads) k3_simt_act_kernel(const T* __restri
         for (int i = 0; i < kPerD; ++i) {
             const int e = tid + i * kThreads;
             const int m = m0 + e / kStep, n = n0 + e % kStep;
-            dreg[i] = (m < M && n < N) ? ActIO<T>::to_f(dY[static_cast<size_t>(m) * N + n]) : 0.f;
+            dreg[i] = (m < M && n < nend) ? ActIO<T>::to_f(dY[static_cast<size_t>(m) * N + n]) : 0.f;
         }
         const int n = n0 + wn;
         wreg = make_uint2(0u, 0u);
         wscale = 0.f;
-        if (n < N && k0 + wk < K) {  // K is a multiple of 16
+        if (n < nend && k0 + wk < K) {  // K is a multiple of 16
             wscale = __ldg(sw + n);
             if constexpr (W4)
                 wreg.x = __ldg(reinterpret_cast<const uint32_t*>(Wq + (static_cast<size_t>(n) * K + k0 + wk) / 2));
@@ -80,12 +85,12 @@ __global__ void __launch_bounds__(kThreads) k3_simt_act_kernel(const T* __restri
         }
     };
     float acc[TM][4] = {};
-    fetch(0);
+    fetch(nbeg);
     put(0);
     __syncthreads();
     int b = 0;
-    for (int n0 = 0; n0 < N; n0 += kStep, b ^= 1) {
-        const bool more = n0 + kStep < N;
+    for (int n0 = nbeg; n0 < nend; n0 += kStep, b ^= 1) {
+        const bool more = n0 + kStep < nend;
         if (more) fetch(n0 + kStep);
 #pragma unroll 8
         for (int n = 0; n < kStep; ++n) {
@@ -101,6 +106,30 @@ __global__ void __launch_bounds__(kThreads) k3_simt_act_kernel(const T* __restri
         }
         if (more) put(b ^ 1);
         __syncthreads();
+    }
+    if (S > 1) {
+        // partial tiles [kRows][kCols] in the buffers that the products are done with
+        float* part = &sW[0][0][0];
+        static_assert(sizeof(sW) >= kRows * kCols * sizeof(float), "partial tile");
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            *reinterpret_cast<float4*>(part + (ty + 16 * i) * kCols + 4 * tx) =
+                make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        cluster_arrive();
+        cluster_wait();
+        if (split == 0) {
+            for (int q = 1; q < S; ++q) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const uint32_t at = dsmem_addr(part + (ty + 16 * i) * kCols + 4 * tx, static_cast<uint32_t>(q));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][e] += __uint_as_float(dsmem_ld_u32(at + 4u * e));
+                }
+            }
+        }
+        cluster_arrive();  // the partial tiles may go
+        cluster_wait();
+        if (split != 0) return;
     }
     for (int i = tid; i < kRows * ep.r; i += kThreads) {
         const int mm = i / ep.r, j = i - mm * ep.r;
@@ -140,13 +169,17 @@ __global__ void __launch_bounds__(kThreads) k3_simt_act_kernel(const T* __restri
 template <typename T, bool W4>
 cudaError_t run(const T* dY, const uint8_t* Wq, const float* sw, int M, int N, int K, const DxEpilogue& ep,
                 cudaStream_t s) {
-    // 64-row tiles where they fill the machine, else 32
+    // 64-row tiles where they fill the machine, else 32, and the contraction
+    // split while that leaves SMs idle and a CTA at least two steps
     const int across = (K + kCols - 1) / kCols;
     if (static_cast<long long>((M + 63) / 64) * across >= 2 * sm_count())
         return launch_k(k3_simt_act_kernel<T, W4, 4>, dim3(across, (M + 63) / 64), dim3(kThreads), 0, s, 1, dY, Wq, sw,
-                        M, N, K, ep);
-    return launch_k(k3_simt_act_kernel<T, W4, 2>, dim3(across, (M + 31) / 32), dim3(kThreads), 0, s, 1, dY, Wq, sw, M,
-                    N, K, ep);
+                        M, N, K, 1, ep);
+    const int down = (M + 31) / 32, steps = (N + kStep - 1) / kStep;
+    int S = 1;
+    while (S < 8 && 2 * S * across * down <= sm_count() && 4 * S <= steps) S *= 2;
+    return launch_kx(k3_simt_act_kernel<T, W4, 2>, dim3(across * S, down), dim3(kThreads), 0, s, S, dY, Wq, sw, M, N, K,
+                     S, ep);
 }
 
 }  // namespace

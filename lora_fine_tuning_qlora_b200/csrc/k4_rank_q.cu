@@ -66,7 +66,9 @@ __device__ __forceinline__ int column_exponent(uint32_t top) {
 
 // The four digits of v 2^p, lowest first.
 __device__ __forceinline__ void make_digits(float v, int p, int (&d)[4]) {
-    int t = __float2int_rn(scalbnf(v, p));
+    // v 2^p in two exact steps (-98 <= p <= 155)
+    const int h = p / 2;
+    int t = __float2int_rn(v * __int_as_float((h + 127) << 23) * __int_as_float((p - h + 127) << 23));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         d[i] = i < 3 ? static_cast<int>(static_cast<int8_t>(t & 0xFF)) : t;
@@ -86,17 +88,19 @@ __global__ void __launch_bounds__(kPrepThreads) k4_q_digits_kernel(const float* 
     uint32_t CL;
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(CL));
     const int tid = threadIdx.x;
-    const size_t n = static_cast<size_t>(M) * r;
-    const size_t step = static_cast<size_t>(CL) * kPrepThreads;
+    // (M r < 2^27, and the digit words of all tiles < 2^25: 32-bit indices)
+    const uint32_t n = static_cast<uint32_t>(M) * static_cast<uint32_t>(r);
+    const uint32_t step = CL * kPrepThreads;
     pdl_trigger();
     if (tid < 64) top[tid] = 0u;
     __syncthreads();
     pdl_wait();
-    auto value = [&](size_t m, int j) {
-        return sum_slices(G + m * r + j, n, nsl) * __ldg(sx + m);
+    auto value = [&](uint32_t m, int j) {
+        const float g = nsl == 1 ? __ldg(G + m * r + j) : sum_slices(G + m * r + j, n, nsl);
+        return g * __ldg(sx + m);
     };
-    for (size_t i = rank * kPrepThreads + tid; i < n; i += step) {
-        const size_t m = i / r;
+    for (uint32_t i = rank * kPrepThreads + tid; i < n; i += step) {
+        const uint32_t m = i / static_cast<uint32_t>(r);
         const int j = static_cast<int>(i - m * r);
         atomicMax(&top[j], __float_as_uint(value(m, j)) & 0x7FFFFFFFu);
     }
@@ -113,26 +117,26 @@ __global__ void __launch_bounds__(kPrepThreads) k4_q_digits_kernel(const float* 
     __syncthreads();
     const int RP = ceil4(r);
     const int tiles = (M + kRows - 1) / kRows;
-    const size_t items = static_cast<size_t>(tiles) * RP * (kRows / 4);
-    for (size_t i = rank * kPrepThreads + tid; i < items; i += step) {
-        const int j = static_cast<int>(i % RP);
-        const size_t rest = i / RP;
+    const uint32_t items = static_cast<uint32_t>(tiles) * RP * (kRows / 4);
+    for (uint32_t i = rank * kPrepThreads + tid; i < items; i += step) {
+        const uint32_t rest = i / static_cast<uint32_t>(RP);
+        const int j = static_cast<int>(i - rest * RP);
         const int g = static_cast<int>(rest % (kRows / 4));
-        const size_t tile = rest / (kRows / 4);
+        const uint32_t tile = rest / (kRows / 4);
         uint32_t w[4] = {0u, 0u, 0u, 0u};
         const int p = j < r ? pexp[j] : kExpNaN;
         if (p != kExpNaN) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const size_t m = tile * kRows + 4 * g + e;
-                if (m >= static_cast<size_t>(M)) continue;
+                const uint32_t m = tile * kRows + 4 * g + e;
+                if (m >= static_cast<uint32_t>(M)) continue;
                 int dg[4];
                 make_digits(value(m, j), p, dg);
 #pragma unroll
                 for (int d = 0; d < 4; ++d) w[d] |= (static_cast<uint32_t>(dg[d]) & 0xFFu) << (8 * e);
             }
         }
-        uint8_t* tab = digits + kExpBytes + tile * (static_cast<size_t>(4 * RP) * kRows);
+        uint8_t* tab = digits + kExpBytes + static_cast<size_t>(tile) * (4 * RP * kRows);
 #pragma unroll
         for (int d = 0; d < 4; ++d)
             *reinterpret_cast<uint32_t*>(tab + digit_off(d * RP + j, 4 * g)) = w[d];

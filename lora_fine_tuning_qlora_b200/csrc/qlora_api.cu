@@ -543,7 +543,7 @@ static int dx_epilogue(const qlora_dx_epilogue* x, DxEpilogue& ep) {
 static int gemm_dx_impl(const qlora_layer_desc* d, int M, const void* dY, const int8_t* Wq,
                         const float* sw, const float* A, const void* gate, void* dX,
                         const void* workspace, size_t workspace_bytes, void* stream,
-                        bool w4 = false, const qlora_dx_epilogue* x = nullptr) {
+                        bool w4 = false, const qlora_dx_epilogue* x = nullptr, bool dense_ready = false) {
     int rc = check_layer(d, M);
     if (rc != QLORA_OK) return rc;
     QL_REQUIRE(!w4 || d->K % 32 == 0, QLORA_EUNSUPPORTED,
@@ -573,8 +573,9 @@ static int gemm_dx_impl(const qlora_layer_desc* d, int M, const void* dY, const 
     if (dense && workspace_bytes >= dense_at + dense) {
         // (the calls that pass an epilogue take a writable workspace)
         uint8_t* Wd = const_cast<uint8_t*>(static_cast<const uint8_t*>(workspace)) + dense_at;
-        rc = cuda_status(launch_dequantize(Wq, sw, d->N, d->K, w4, Wd, static_cast<cudaStream_t>(stream)),
-                         "de-quantize launch");
+        if (!dense_ready)
+            rc = cuda_status(launch_dequantize(Wq, sw, d->N, d->K, w4, Wd, static_cast<cudaStream_t>(stream)),
+                             "de-quantize launch");
         if (rc != QLORA_OK) return rc;
         return cuda_status(launch_gemm_dx_dense(dY, Wd, M, d->N, d->K, ep, status, static_cast<cudaStream_t>(stream)),
                            "dX GEMM launch");
@@ -675,10 +676,12 @@ int qlora_forward(const qlora_layer_desc* d, int M, const void* X, const int8_t*
 // global-mode stream capture) the backward stays on the caller's stream.
 namespace {
 constexpr int kSideStreamMinM = 512;
+constexpr double kSideStreamMinWork = 268435456.0;  // M K N, qlora_backward_ckpt
 struct SideStream {
     bool tried = false;
     cudaStream_t st = nullptr;
     cudaEvent_t fork = nullptr, join = nullptr;
+    cudaEvent_t start = nullptr, dense = nullptr;  // qlora_backward_ckpt: de-quantize beside the dY pass
 };
 SideStream* side_stream() {
     static thread_local SideStream per_dev[64];
@@ -689,7 +692,9 @@ SideStream* side_stream() {
         ss.tried = true;
         if (cudaStreamCreateWithFlags(&ss.st, cudaStreamNonBlocking) != cudaSuccess ||
             cudaEventCreateWithFlags(&ss.fork, cudaEventDisableTiming) != cudaSuccess ||
-            cudaEventCreateWithFlags(&ss.join, cudaEventDisableTiming) != cudaSuccess) {
+            cudaEventCreateWithFlags(&ss.join, cudaEventDisableTiming) != cudaSuccess ||
+            cudaEventCreateWithFlags(&ss.start, cudaEventDisableTiming) != cudaSuccess ||
+            cudaEventCreateWithFlags(&ss.dense, cudaEventDisableTiming) != cudaSuccess) {
             (void)cudaGetLastError();
             ss.st = nullptr;
         }
@@ -827,14 +832,37 @@ int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, cons
         return rc;
     }
     QL_REQUIRE(workspace_bytes >= qlora_ckpt_workspace_bytes(d, M), QLORA_EINVAL, "workspace too small");
+    // The second stream, as in qlora_backward, where the dX GEMM outlasts the
+    // fork and the join (about 10 us with their host calls)
+    const bool large = M >= kSideStreamMinM && static_cast<double>(M) * d->K * d->N >= kSideStreamMinWork;
+    SideStream* ss = dX && large ? side_stream() : nullptr;
+    const size_t dense = ss ? dx_dense_bytes(act_of(d), M, d->N, d->K, d->r) : 0;
+    if (dense) {
+        // the kernel's de-quantization needs nothing of the dY pass: beside it
+        uint8_t* Wd = static_cast<uint8_t*>(workspace) + ckpt_dense_offset(d, M);
+        rc = cuda_status(cudaEventRecord(ss->start, s), "backward fork");
+        if (rc == QLORA_OK) rc = cuda_status(cudaStreamWaitEvent(ss->st, ss->start, 0), "backward fork");
+        if (rc != QLORA_OK) return rc;
+        const int rc_w = cuda_status(launch_dequantize(Wq, sw, d->N, d->K, false, Wd, ss->st), "de-quantize launch");
+        rc = cuda_status(cudaEventRecord(ss->dense, ss->st), "backward join");
+        if (rc != QLORA_OK) return rc;
+        if (rc_w != QLORA_OK) {
+            (void)cudaStreamWaitEvent(s, ss->dense, 0);
+            return rc_w;
+        }
+    }
     rc = lora_grad_dy_impl(d, M, dY, B, xA, dB, dbias, nullptr, workspace, workspace_bytes, stream, true);
+    if (dense) {  // whatever happened, the caller's stream never runs ahead of the second one
+        const int rc_d = cuda_status(cudaStreamWaitEvent(s, ss->dense, 0), "backward join");
+        if (rc == QLORA_OK) rc = rc_d;
+    }
     if (rc != QLORA_OK) return rc;
-    SideStream* ss = (dX && M >= kSideStreamMinM) ? side_stream() : nullptr;
     if (ss) {
-        // as qlora_backward: the X pass beside the dX GEMM
+        // the X pass beside the dX GEMM
         rc = cuda_status(cudaEventRecord(ss->fork, s), "backward fork");
         if (rc != QLORA_OK) return rc;
-        rc = gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, &none_or);
+        rc = gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, &none_or,
+                          dense != 0);
         const int rc_wait = cuda_status(cudaStreamWaitEvent(ss->st, ss->fork, 0), "backward fork");
         const int rc_x = rc_wait == QLORA_OK ? grad_x_ckpt(d, M, Xq, sx, dA, workspace, ss->st) : rc_wait;
         const int rc_join = cuda_status(cudaEventRecord(ss->join, ss->st), "backward join");

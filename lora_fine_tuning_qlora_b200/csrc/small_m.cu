@@ -45,6 +45,7 @@ constexpr int kFwdThreads = 32 * (2 + kEpiW);
 constexpr int kDxThreads = 32 * (2 + kDqW + kEpiW);
 constexpr int kMaxSplit = 8;
 constexpr int kMaxTokens = 64;           // above this the large-tile kernels measured as fast or faster
+constexpr int kMaxTokensEx = 256;        // (EX) ... unless their tiles are few: one MMA's N
 
 struct SmallArgs {
     int M, N, K;          // the layer's shapes (tokens, out_features, in_features)
@@ -560,7 +561,16 @@ int pick_split(int tiles, int kblocks) {
 
 }  // namespace
 
-bool small_m_applies(int M, int out_channels, int r) {
+bool small_m_applies(int M, int out_channels, int r, int contraction, bool ex) {
+    if (ex && M > kMaxTokens && M <= kMaxTokensEx && r <= 16) {
+        // up to 256 tokens where the large tiles, 128 x 64 or more, would be few
+        // and their contraction long: split over a cluster, it ends sooner (the
+        // backward of 202 tokens, K 80, N 12608: 72 -> 60 us; 177 tokens, K
+        // 432, N 10488: 69 -> 55 us)
+        const int tiles = ((M + 127) / 128) * ((out_channels + 63) / 64);
+        const int mine = (out_channels + kCh - 1) / kCh;
+        return mine * kMaxSplit <= sm_count() && 4 * tiles <= sm_count() && contraction >= 1024;
+    }
     if (M < 1 || M > kMaxTokens || r > 16) return false;
     // only where the large-tile kernels leave SMs idle
     return ((M + 127) / 128) * ((out_channels + 127) / 128) < sm_count();

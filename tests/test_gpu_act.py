@@ -60,7 +60,7 @@ def run_forward(M, K, N, r, dt, name, residual, save, seed=0, **kw):
 FORWARD = [
     (1, 2048, 1000, 4), (1, 16, 1, 1), (7, 784, 130, 3), (16, 4096, 512, 4), (17, 96, 33, 8), (64, 528, 257, 16),
     (65, 784, 128, 4), (100, 4096, 128, 8), (130, 2048, 200, 16), (333, 784, 1001, 8), (300, 272, 96, 20),
-    (128, 144, 40, 64), (513, 1040, 3000, 4), (2048, 272, 2600, 4), (2050, 512, 2568, 16), (1600, 256, 3333, 8),
+    (128, 144, 40, 64), (250, 4112, 70, 4), (513, 1040, 3000, 4), (2048, 272, 2600, 4), (2050, 512, 2568, 16), (1600, 256, 3333, 8),
 ]
 
 
@@ -104,7 +104,7 @@ def run_backward(M, K, N, r, dt, name, add, seed=0, z=None, dY=None, want_dx=Tru
 BACKWARD = [
     (1, 16, 8, 1), (1, 2048, 512, 4), (16, 1024, 2048, 4), (17, 784, 136, 3), (64, 528, 264, 16), (65, 784, 128, 4),
     (127, 48, 64, 8), (129, 272, 200, 16), (333, 784, 1000, 8), (300, 272, 96, 20), (140, 144, 40, 33),
-    (256, 144, 72, 64), (77, 160, 10, 4), (1024, 2576, 128, 4), (1030, 2560, 192, 16), (2500, 528, 320, 8),
+    (256, 144, 72, 64), (77, 160, 10, 4), (202, 80, 12608, 4), (256, 48, 2048, 16), (70, 2048, 1032, 8), (1024, 2576, 128, 4), (1030, 2560, 192, 16), (2500, 528, 320, 8),
 ]
 
 
