@@ -511,9 +511,8 @@ size_t qlora_ckpt_scales(int rows, int cols);
 size_t qlora_ckpt_workspace_bytes(const qlora_layer_desc* d, int M);
 
 /* a5 from the kept codes: dA = c * (Xq sx)^T G [K,r], G from the workspace
- * that a3 filled; overwrites the workspace behind qlora_workspace_bytes (of
- * qlora_ckpt_workspace_bytes in all, or at least the digits: 256 + 512
- * ceil4(r) ceil(M / 128) bytes rounded up to 256).  The sum over the rows runs in integers (sx G as a 31-bit fixed-point value per
+ * that a3 filled; overwrites the workspace (of qlora_ckpt_workspace_bytes)
+ * behind qlora_workspace_bytes.  The sum over the rows runs in integers (sx G as a 31-bit fixed-point value per
  * column of G): dA does not depend on how it is split.  A column of G that
  * holds an infinity or a NaN gives NaN in that column of dA.  At most 1047552
  * rows (QLORA_EUNSUPPORTED). */
@@ -525,7 +524,7 @@ int qlora_lora_grad_x_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, c
  * added) and qlora_lora_grad_x_ckpt.  In bf16 the factors B and xA of the dY
  * pass enter at 24 bits for r <= 32 (16 in qlora_backward and for larger r).
  * Workspace of qlora_ckpt_workspace_bytes; streams and capture as
- * qlora_backward, the second stream from 512 tokens and M K N >= 2^28, also for
+ * qlora_backward, the second stream from 512 tokens and M K N >= 2^32, also for
  * the kernel's de-quantization beside the dY pass.  Deterministic. */
 int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx, const void* dY,
                         const int8_t* Wq, const float* sw, const float* A, const float* B, const float* xA,

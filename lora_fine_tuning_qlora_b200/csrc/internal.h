@@ -211,9 +211,9 @@ cudaError_t launch_rank_dy_tc(const void* dY, const float* B, const float* xA, i
 cudaError_t launch_rank_x_tc(const void* X, const float* G, int nsl, int M, int K, int r, float c,
                              float* dA, int* status, cudaStream_t s);
 
-// dA = c X^T G from the input kept as row codes, X = Xq sx (k4_rank_q.cu): a
-// pass that turns sx G into 8-bit digits in `digits`, then the column sums of
-// Xq on the int8 tensor cores.  M at most kRankQMaxRows.
+// dA = c X^T G from the input kept as row codes, X = Xq sx (k4_rank_q.cu): sx G
+// as 8-bit digits in `digits` (rank_q_digit_bytes, 256-byte aligned), then the
+// column sums of Xq on the int8 tensor cores.  M at most kRankQMaxRows.
 constexpr int kRankQMaxRows = 8 * 1023 * 128;
 size_t rank_q_digit_bytes(int M, int r);
 cudaError_t launch_rank_x_q(const int8_t* Xq, const float* sx, const float* G, int nsl, int M, int K, int r,

@@ -18,16 +18,18 @@
 // Bound by reading the codes once: M K bytes, half of a bf16 input.  The
 // codes need no conversion on the way: a TMA box of 128 rows x 128 columns
 // (128-byte swizzle) is the MN-major A operand (M = 128 columns, K = 32 rows
-// per MMA) as it lands.  The digits of a 128-row tile are prepared once by
-// the digit kernel in the K-major table layout the MMA reads, so every CTA
-// only copies 512 ceil4(r) bytes of them beside each 16 KB tile.
+// per MMA) as it lands.  The digits of a 128-row tile are prepared once, by two
+// small kernels (V with its columns' maxima; the digits), in the K-major table
+// layout the MMA reads, so every CTA only copies 512 ceil4(r) bytes of them
+// beside each 16 KB tile.  16384 x 4096 codes at rank 4: 19 us, 3.5 TB/s (the
+// bf16 input's pass: 28.7 us alone).
 //
 // Rows are split over a cluster of CL <= 8 CTAs per 128-column block, whose
 // partial sums meet in the shared memory of the CTA that owns the column, as
 // int64.  Warps: 0 producer, 1 TMEM owner and MMA issuer, 2..5 read-out.
 //
-// Up to 128 rows (one tile) there is no digit kernel: warps 2..5 of every CTA
-// make the tile's table themselves, a launch less.
+// Up to 128 rows (one tile) there are no such kernels: warps 2..5 of every CTA
+// make the tile's table themselves, two launches less.
 #include "internal.h"
 #include "ptx.cuh"
 #include "tile_epilogue.cuh"
@@ -44,7 +46,8 @@ constexpr int kThreads = 32 * 6;
 constexpr int kMaxCl = 8;
 constexpr int kMaxTilesPerCta = 1023;             // 1023 * 128 * 128 * 128 < 2^31
 constexpr int kMaxStages = 8;
-constexpr int kPrepThreads = 1024;
+constexpr int kPrepThreads = 256;
+constexpr int kPrepCtas = 64;                     // of the scaling pass, at most
 
 __host__ __device__ constexpr int ceil4(int r) { return (r + 3) / 4 * 4; }
 
@@ -76,50 +79,57 @@ __device__ __forceinline__ void make_digits(float v, int p, int (&d)[4]) {
     }
 }
 
-// One cluster.  Two sweeps over G: the columns' maxima of |V|, then the
-// digits.  (Latency-bound: at 16384 rows and rank 4 each of the 8192 threads
-// takes 8 elements; beside the dX GEMM it is hidden.)
-__global__ void __launch_bounds__(kPrepThreads) k4_q_digits_kernel(const float* __restrict__ G, int nsl,
-                                                                   const float* __restrict__ sx, int M, int r,
-                                                                   uint8_t* __restrict__ digits) {
+// V = sx G [M, r] and, per CTA, its columns' largest magnitudes part[CTA][64].
+// A thread takes a row, so that a warp reduction per column replaces the
+// shared-memory atomics of its 32 rows (with those, and both sweeps on one
+// cluster of eight CTAs, the digits of 11416 rows at rank 8 took 38 us).
+__global__ void __launch_bounds__(kPrepThreads) k4_q_scale_kernel(const float* __restrict__ G, int nsl,
+                                                                  const float* __restrict__ sx, int M, int r,
+                                                                  float* __restrict__ V, uint32_t* __restrict__ part) {
     __shared__ uint32_t top[64];
-    __shared__ int pexp[64];
-    const uint32_t rank = cluster_ctarank();
-    uint32_t CL;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(CL));
-    const int tid = threadIdx.x;
-    // (M r < 2^27, and the digit words of all tiles < 2^25: 32-bit indices)
-    const uint32_t n = static_cast<uint32_t>(M) * static_cast<uint32_t>(r);
-    const uint32_t step = CL * kPrepThreads;
+    const int tid = threadIdx.x, lane = tid & 31;
     pdl_trigger();
     if (tid < 64) top[tid] = 0u;
     __syncthreads();
     pdl_wait();
-    auto value = [&](uint32_t m, int j) {
-        const float g = nsl == 1 ? __ldg(G + m * r + j) : sum_slices(G + m * r + j, n, nsl);
-        return g * __ldg(sx + m);
-    };
-    for (uint32_t i = rank * kPrepThreads + tid; i < n; i += step) {
-        const uint32_t m = i / static_cast<uint32_t>(r);
-        const int j = static_cast<int>(i - m * r);
-        atomicMax(&top[j], __float_as_uint(value(m, j)) & 0x7FFFFFFFu);
+    const size_t slice = static_cast<size_t>(M) * r;
+    for (int m0 = blockIdx.x * kPrepThreads; m0 < M; m0 += gridDim.x * kPrepThreads) {
+        const int m = m0 + tid;
+        const float s = m < M ? __ldg(sx + m) : 0.f;
+        const size_t at = static_cast<size_t>(m < M ? m : 0) * r;
+        for (int j = 0; j < r; ++j) {
+            const float g = nsl == 1 ? __ldg(G + at + j) : sum_slices(G + at + j, slice, nsl);
+            const float v = m < M ? g * s : 0.f;
+            if (m < M) V[at + j] = v;
+            const uint32_t t = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu);
+            if (lane == 0) atomicMax(&top[j], t);
+        }
     }
     __syncthreads();
-    cluster_arrive();
-    cluster_wait();
+    if (tid < 64) part[blockIdx.x * 64 + tid] = top[tid];
+}
+
+// The columns' exponents from the `ctas` partial maxima, and the digit tables.
+__global__ void __launch_bounds__(kPrepThreads) k4_q_digits_kernel(const float* __restrict__ V,
+                                                                   const uint32_t* __restrict__ part, int ctas, int M,
+                                                                   int r, uint8_t* __restrict__ digits) {
+    __shared__ int pexp[64];
+    const int tid = threadIdx.x;
+    pdl_trigger();
+    pdl_wait();
     if (tid < 64) {
         uint32_t t = 0;
-        for (uint32_t q = 0; q < CL; ++q) t = max(t, dsmem_ld_u32(dsmem_addr(&top[tid], q)));
-        const int p = column_exponent(t);
-        pexp[tid] = p;
-        if (rank == 0) reinterpret_cast<int*>(digits)[tid] = p;
+        for (int q = 0; q < ctas; ++q) t = max(t, __ldg(part + q * 64 + tid));
+        pexp[tid] = column_exponent(t);
+        if (blockIdx.x == 0) reinterpret_cast<int*>(digits)[tid] = pexp[tid];
     }
     __syncthreads();
-    const int RP = ceil4(r);
-    const int tiles = (M + kRows - 1) / kRows;
-    const uint32_t items = static_cast<uint32_t>(tiles) * RP * (kRows / 4);
-    for (uint32_t i = rank * kPrepThreads + tid; i < items; i += step) {
-        const uint32_t rest = i / static_cast<uint32_t>(RP);
+    // one word (four rows) of each of the four digits an item; the items of
+    // all tiles are fewer than 2^25
+    const uint32_t RP = static_cast<uint32_t>(ceil4(r));
+    const uint32_t items = static_cast<uint32_t>((M + kRows - 1) / kRows) * RP * (kRows / 4);
+    for (uint32_t i = blockIdx.x * kPrepThreads + tid; i < items; i += gridDim.x * kPrepThreads) {
+        const uint32_t rest = i / RP;
         const int j = static_cast<int>(i - rest * RP);
         const int g = static_cast<int>(rest % (kRows / 4));
         const uint32_t tile = rest / (kRows / 4);
@@ -131,7 +141,7 @@ __global__ void __launch_bounds__(kPrepThreads) k4_q_digits_kernel(const float* 
                 const uint32_t m = tile * kRows + 4 * g + e;
                 if (m >= static_cast<uint32_t>(M)) continue;
                 int dg[4];
-                make_digits(value(m, j), p, dg);
+                make_digits(__ldg(V + static_cast<size_t>(m) * r + j), p, dg);
 #pragma unroll
                 for (int d = 0; d < 4; ++d) w[d] |= (static_cast<uint32_t>(dg[d]) & 0xFFu) << (8 * e);
             }
@@ -139,11 +149,8 @@ __global__ void __launch_bounds__(kPrepThreads) k4_q_digits_kernel(const float* 
         uint8_t* tab = digits + kExpBytes + static_cast<size_t>(tile) * (4 * RP * kRows);
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-            *reinterpret_cast<uint32_t*>(tab + digit_off(d * RP + j, 4 * g)) = w[d];
+            *reinterpret_cast<uint32_t*>(tab + digit_off(d * static_cast<int>(RP) + j, 4 * g)) = w[d];
     }
-    // no CTA leaves while another reads its maxima
-    cluster_arrive();
-    cluster_wait();
 }
 
 struct RankQArgs {
@@ -356,8 +363,13 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
 
 }  // namespace
 
-size_t rank_q_digit_bytes(int M, int r) {
+// The exponents and tables; behind them the partial maxima and V.
+static size_t digit_table_bytes(int M, int r) {
     return kExpBytes + static_cast<size_t>((M + kRows - 1) / kRows) * 4 * ceil4(r) * kRows;
+}
+
+size_t rank_q_digit_bytes(int M, int r) {
+    return digit_table_bytes(M, r) + kPrepCtas * 64 * 4 + static_cast<size_t>(M) * r * 4;
 }
 
 cudaError_t launch_rank_x_q(const int8_t* Xq, const float* sx, const float* G, int nsl, int M, int K, int r,
@@ -366,12 +378,17 @@ cudaError_t launch_rank_x_q(const int8_t* Xq, const float* sx, const float* G, i
     const bool own = M <= kRows;
     cudaError_t e = cudaSuccess;
     if (!own) {
-        // digits: a cluster of CTAs, about 8 elements a thread
-        const size_t n = static_cast<size_t>(M) * r;
-        int pc = 1;
-        while (pc < 8 && n > static_cast<size_t>(pc) * kPrepThreads * 8) pc *= 2;
-        e = launch_k(k4_q_digits_kernel, dim3(1, pc), dim3(kPrepThreads), 0, s, pc, G, nsl, sx, M, r,
-                     static_cast<uint8_t*>(digits));
+        uint8_t* buf = static_cast<uint8_t*>(digits);
+        uint32_t* part = reinterpret_cast<uint32_t*>(buf + digit_table_bytes(M, r));
+        float* V = reinterpret_cast<float*>(part + kPrepCtas * 64);
+        const int want = (M + kPrepThreads - 1) / kPrepThreads;
+        const int ctas = want < kPrepCtas ? want : kPrepCtas;
+        e = launch_k(k4_q_scale_kernel, dim3(ctas), dim3(kPrepThreads), 0, s, 1, G, nsl, sx, M, r, V, part);
+        if (e != cudaSuccess) return e;
+        const size_t items = static_cast<size_t>((M + kRows - 1) / kRows) * ceil4(r) * (kRows / 4);
+        const size_t blocks = (items + kPrepThreads - 1) / kPrepThreads, cap = 2 * static_cast<size_t>(sm_count());
+        e = launch_k(k4_q_digits_kernel, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(kPrepThreads), 0,
+                     s, 1, static_cast<const float*>(V), static_cast<const uint32_t*>(part), ctas, M, r, buf);
         if (e != cudaSuccess) return e;
     }
     CUtensorMap tm;

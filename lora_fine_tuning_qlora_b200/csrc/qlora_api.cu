@@ -676,7 +676,7 @@ int qlora_forward(const qlora_layer_desc* d, int M, const void* X, const int8_t*
 // global-mode stream capture) the backward stays on the caller's stream.
 namespace {
 constexpr int kSideStreamMinM = 512;
-constexpr double kSideStreamMinWork = 268435456.0;  // M K N, qlora_backward_ckpt
+constexpr double kSideStreamMinWork = 4294967296.0;  // M K N, qlora_backward_ckpt
 struct SideStream {
     bool tried = false;
     cudaStream_t st = nullptr;
@@ -832,8 +832,8 @@ int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, cons
         return rc;
     }
     QL_REQUIRE(workspace_bytes >= qlora_ckpt_workspace_bytes(d, M), QLORA_EINVAL, "workspace too small");
-    // The second stream, as in qlora_backward, where the dX GEMM outlasts the
-    // fork and the join (about 10 us with their host calls)
+    // The second stream, as in qlora_backward, where the GPU's time (not the
+    // host's, to which the four events add about 15 us) sets the call's pace
     const bool large = M >= kSideStreamMinM && static_cast<double>(M) * d->K * d->N >= kSideStreamMinWork;
     SideStream* ss = dX && large ? side_stream() : nullptr;
     const size_t dense = ss ? dx_dense_bytes(act_of(d), M, d->N, d->K, d->r) : 0;
