@@ -57,6 +57,21 @@ __device__ __forceinline__ void store_block(uint8_t* stg, const float (&v)[kEpiC
                 make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
     __syncwarp();
+    if (!vec) {
+        // rows of any alignment: element by element, 16 neighbouring lanes
+        // along a row (four elements of 8 rows at a time touched eight times
+        // the sectors)
+#pragma unroll
+        for (int it = 0; it < 16; ++it) {
+            const int rr = 2 * it + (lane >> 4), cc = lane & 15;
+            const int gr = row0 + rr, gn = n + cc;
+            if (gr < M && gr >= row_min && gn < N)
+                out[static_cast<size_t>(gr) * ldo + gn] =
+                    *reinterpret_cast<const OutT*>(stg + rr * P + cc * static_cast<int>(sizeof(OutT)));
+        }
+        __syncwarp();
+        return;
+    }
     constexpr int kChunks = kEpiCols * static_cast<int>(sizeof(OutT)) / 16;  // per row
     constexpr int kRowsPerIt = 32 / kChunks;
     constexpr int kElems = 16 / static_cast<int>(sizeof(OutT));              // per chunk
@@ -69,7 +84,7 @@ __device__ __forceinline__ void store_block(uint8_t* stg, const float (&v)[kEpiC
         if (gr < M && gr >= row_min && gn < N) {
             const uint4 val = *reinterpret_cast<const uint4*>(stg + rr * P + ch * 16);
             OutT* dst = out + static_cast<size_t>(gr) * ldo + gn;
-            if (vec && gn + kElems <= N) {
+            if (gn + kElems <= N) {
                 *reinterpret_cast<uint4*>(dst) = val;
             } else {
                 const OutT* e = reinterpret_cast<const OutT*>(&val);
