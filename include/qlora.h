@@ -478,7 +478,8 @@ int qlora_gemm_forward_act_int4(const qlora_layer_desc* d, int M, const int8_t* 
                                 const float* B, const qlora_fwd_epilogue* epilogue, void* Y, void* stream);
 
 /* qlora_quantize_input into the caller's Xq [M,K] (16-byte aligned), sx [M]
- * and xA [M,r], then qlora_gemm_forward_act.  Xq, sx and xA are the layer's
+ * and xA [M,r] (the same codes and scales; at some sizes the fp32 sums of xA
+ * are grouped differently), then qlora_gemm_forward_act.  Xq, sx and xA are the layer's
  * checkpoint for qlora_backward_ckpt: nothing else of the forward has to be
  * kept.  No workspace. */
 int qlora_forward_act(const qlora_layer_desc* d, int M, const void* X, const int8_t* Wq, const float* sw,
