@@ -207,7 +207,11 @@ cudaError_t launch_rank_x(Act act, const void* X, const float* G, int nsl, int M
 int rank_tc_col_blocks(int C);
 cudaError_t launch_rank_dy_tc(const void* dY, const float* B, const float* xA, int M, int N, int r,
                               float c, float* Gp, float* dB, float* dbias, int* status,
-                              cudaStream_t s, bool precise = false);
+                              cudaStream_t s);
+// The whole dY pass with the factors at fp32 precision (k4_dy_precise.cu).
+constexpr int kMaxPreciseR = 32;
+cudaError_t launch_dy_precise(const void* dY, const float* B, const float* xA, int M, int N, int r, float c, float* Gp,
+                              float* dB, float* dbias, int* status, cudaStream_t s);
 cudaError_t launch_rank_x_tc(const void* X, const float* G, int nsl, int M, int K, int r, float c,
                              float* dA, int* status, cudaStream_t s);
 

@@ -500,8 +500,12 @@ __global__ void __launch_bounds__(k2_threads<W4>(), 1)
                     for (int h = 0; h < 2; ++h) {
 #pragma unroll
                         for (int e = 0; e < kEpiCols; ++e) y[e] = z[h * kEpiCols + e];
-                        store_block<OutT>(stg, y, lane, Y, static_cast<size_t>(N), row0, row_lim,
-                                          n0 + col + h * kEpiCols, N, vec, row_min);
+                        if (vec)
+                            store_block<OutT>(stg, y, lane, Y, static_cast<size_t>(N), row0, row_lim,
+                                              n0 + col + h * kEpiCols, N, true, row_min);
+                        else
+                            store_block_any<OutT>(stg, y, lane, Y, static_cast<size_t>(N), row0, row_lim,
+                                                  n0 + col + h * kEpiCols, N, row_min);
                     }
                 }
             } else {

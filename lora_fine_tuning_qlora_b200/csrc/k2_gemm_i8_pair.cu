@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(q_threads<W4, EX>(), 1)
 #pragma unroll
             for (int j = 0; j < RP; ++j)
                 xa[j] = (row_ok && j < ep.r) ? __ldg(ep.xA + static_cast<size_t>(row) * ep.r + j) * ep.c : 0.f;
+            if constexpr (EX) {
             // y = acc sx sw + bias + c xA B of this lane's row, 16 columns from `col`
             auto finish16 = [&](const uint32_t (&v)[kEpiCols], int col, float* y) {
 #pragma unroll
@@ -319,7 +320,6 @@ __global__ void __launch_bounds__(q_threads<W4, EX>(), 1)
                     y[e] = acc;
                 }
             };
-            if constexpr (EX) {
                 constexpr int kCols = kQN / (kQEpi / 4);  // this warp's columns
                 const int c0 = (ew >> 2) * kCols;
                 const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(ep.res);
@@ -349,8 +349,12 @@ __global__ void __launch_bounds__(q_threads<W4, EX>(), 1)
                     for (int h = 0; h < 2; ++h) {
 #pragma unroll
                         for (int e = 0; e < kEpiCols; ++e) y[e] = z[h * kEpiCols + e];
-                        store_block<__nv_bfloat16>(stg, y, lane, Y, static_cast<size_t>(N), row0, M,
-                                                   n0 + col + h * kEpiCols, N, vec);
+                        if (vec)
+                            store_block<__nv_bfloat16>(stg, y, lane, Y, static_cast<size_t>(N), row0, M,
+                                                       n0 + col + h * kEpiCols, N, true);
+                        else
+                            store_block_any<__nv_bfloat16>(stg, y, lane, Y, static_cast<size_t>(N), row0, M,
+                                                           n0 + col + h * kEpiCols, N);
                     }
                 }
             } else {
@@ -364,7 +368,22 @@ __global__ void __launch_bounds__(q_threads<W4, EX>(), 1)
                 tmem_ld16(tbase + col, v);
                 tmem_ld_wait();
                 float y[kEpiCols];
-                finish16(v, col, y);
+#pragma unroll
+                for (int e = 0; e < kEpiCols; ++e) {
+                    const int c = col + e;
+                    const float a = static_cast<float>(static_cast<int32_t>(v[e]));
+                    float acc = fmaf(a * sxm, sSw[c], sBias[c]);
+                    const float4* b4 = reinterpret_cast<const float4*>(sB + c * RP);
+#pragma unroll
+                    for (int j4 = 0; j4 < RP / 4; ++j4) {
+                        const float4 b = b4[j4];
+                        acc = fmaf(xa[4 * j4 + 0], b.x, acc);
+                        acc = fmaf(xa[4 * j4 + 1], b.y, acc);
+                        acc = fmaf(xa[4 * j4 + 2], b.z, acc);
+                        acc = fmaf(xa[4 * j4 + 3], b.w, acc);
+                    }
+                    y[e] = acc;
+                }
                 if (ep.relu) {
 #pragma unroll
                     for (int e = 0; e < kEpiCols; ++e) y[e] = y[e] > 0.f ? y[e] : 0.f;

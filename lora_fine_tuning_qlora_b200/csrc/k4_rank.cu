@@ -389,8 +389,11 @@ int rank_col_blocks(Act act, int N) {
 cudaError_t launch_rank_dy(Act act, const void* dY, const float* B, const float* xA, int M, int N,
                            int r, float c, float* Gp, float* dB, float* dbias, int* status,
                            cudaStream_t s, bool precise) {
-    if (rank_dy_tc(act, N))
-        return launch_rank_dy_tc(dY, B, xA, M, N, r, c, Gp, dB, dbias, status, s, precise);
+    if (rank_dy_tc(act, N)) {
+        if (precise && Gp && dB && r <= kMaxPreciseR)
+            return launch_dy_precise(dY, B, xA, M, N, r, c, Gp, dB, dbias, status, s);
+        return launch_rank_dy_tc(dY, B, xA, M, N, r, c, Gp, dB, dbias, status, s);
+    }
     const int cl = cluster_for(M, 4);
     const int RM = (M + cl - 1) / cl;
     const dim3 grid((N + kCols - 1) / kCols, cl);

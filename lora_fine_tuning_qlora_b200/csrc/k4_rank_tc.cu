@@ -30,16 +30,6 @@
 // and remainder halves sit RP = roundup(r, 16) columns apart in TMEM, so one
 // 16-column load of each gives 16 sums.
 //
-// NT = 3 terms (v = hi + mid + lo to 24 bits) carry the factors at fp32
-// precision: the dY pass of the backward from 8-bit checkpoints, ranks up to
-// 32 (beyond, the third tables do not fit beside the tiles).  The terms then
-// sit ceil4(r) columns apart, so that rank 4 and its ones column take one
-// 16-column MMA, and the column sums leave TMEM every kDrain tiles: the
-// tensor cores' fp32 accumulation truncates, which over the 256 products of
-// 4096 rows shrank dB by 4.4e-6 of itself; chains of 32 and fp32 additions of
-// their results (on the operand warps, from the accumulator that the next
-// group's products do not use) leave about a tenth of that.
-//
 // Column sums: the CL <= 8 CTAs that share a column block form a cluster
 // along the rows.  Each CTA owns 128/CL of the block's columns: every CTA
 // stores its partials for those columns into the owner's shared memory
@@ -66,8 +56,6 @@ constexpr int kThreads = 64 + 32 * kWorkers;
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kTabSbo = (kTileCols / 8) * 128;  // 8-row group stride of a 128-wide table
 constexpr int kMaxBulkR = 8;                         // rank limit of the bulk-copied V rows
-constexpr int kDrain = 4;                            // NT = 3: tiles per column accumulator
-constexpr int kMaxPreciseR = 32;                     // rank limit of the three-term tables
 
 // What one launch computes.
 struct Parts {
@@ -93,25 +81,23 @@ struct RankTcArgs {
 // Shared-memory and TMEM layout for rank r (same on host and device).
 struct RtLayout {
     int RP, NG, NV, JP;
-    uint32_t vtab, bcat, recv, bar, vraw, vslot, drain, total;
+    uint32_t vtab, bcat, recv, bar, vraw, vslot, total;
     uint32_t tmem_cols, d_col, g_col;
-    __host__ __device__ RtLayout(Parts p, int r, bool vbulk, int nt) {
-        RP = nt == 3 ? (r + 3) / 4 * 4 : (r + 15) / 16 * 16;
-        NG = p.g ? (nt * RP + 15) / 16 * 16 : 0;
-        NV = p.d ? (nt * RP + (p.ones ? 1 : 0) + 15) / 16 * 16 : 0;
+    __host__ __device__ RtLayout(Parts p, int r, bool vbulk) {
+        RP = (r + 15) / 16 * 16;
+        NG = p.g ? 2 * RP : 0;
+        NV = p.d ? 2 * RP + (p.ones ? 16 : 0) : 0;
         JP = p.d ? r + (p.ones ? 1 : 0) : 0;
         vtab = 2 * kTileBytes;
         bcat = vtab + 2 * static_cast<uint32_t>(NV) * 256;
         recv = bcat + static_cast<uint32_t>(NG) * 256;
         bar = recv + (((kTileCols + kMaxCluster) * JP * 4 + 15) / 16) * 16;
-        vraw = bar + 192;  // [2][128 rows][r] fp32 with vbulk
+        vraw = bar + 128;  // [2][128 rows][r] fp32 with vbulk
         vslot = vbulk ? static_cast<uint32_t>(kTileRows * r * 4) : 0u;
-        drain = vraw + 2 * vslot;  // NT = 3: the columns' sums so far, [128][JP]
-        total = drain + (nt == 3 ? static_cast<uint32_t>(kTileCols * JP * 4) : 0u);
+        total = vraw + 2 * vslot;
         d_col = 0;
-        const int nd = nt == 3 ? 2 * NV : NV;  // NT = 3: two column accumulators in turn
-        g_col = static_cast<uint32_t>(nd);
-        const uint32_t need = static_cast<uint32_t>(nd + 2 * NG);
+        g_col = static_cast<uint32_t>(NV);
+        const uint32_t need = static_cast<uint32_t>(NV + 2 * NG);
         tmem_cols = 32;
         while (tmem_cols < need) tmem_cols <<= 1;
     }
@@ -126,59 +112,20 @@ __device__ __forceinline__ uint32_t ktab_off(int row, int k) {
                                  (k & 7) * 2);
 }
 
-// The NT bf16 terms of v: each the nearest bf16 of what the ones before leave.
-template <int NT>
-__device__ __forceinline__ void split_terms(float v, __nv_bfloat16 (&t)[NT]) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        t[i] = __float2bfloat16_rn(v);
-        v -= __bfloat162float(t[i]);
-    }
+__device__ __forceinline__ void put_split(uint8_t* tab, int row_hi, int row_lo, int k, float v) {
+    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+    const __nv_bfloat16 lo = __float2bfloat16_rn(v - __bfloat162float(hi));
+    *reinterpret_cast<__nv_bfloat16*>(tab + ktab_off(row_hi, k)) = hi;
+    *reinterpret_cast<__nv_bfloat16*>(tab + ktab_off(row_lo, k)) = lo;
 }
 
-// Term i of v into row `row` + i * RP.
-template <int NT>
-__device__ __forceinline__ void put_split(uint8_t* tab, int row, int RP, int k, float v) {
-    __nv_bfloat16 t[NT];
-    split_terms<NT>(v, t);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) *reinterpret_cast<__nv_bfloat16*>(tab + ktab_off(row + i * RP, k)) = t[i];
-}
-
-// sink(j, sum) for the r sums of the NT terms' accumulators, RP TMEM columns apart.
-template <int NT, typename Sink>
-__device__ __forceinline__ void read_sums(uint32_t base, int RP, int r, Sink sink) {
-    if constexpr (NT == 3) {
-        for (int c0 = 0; c0 < r; c0 += 4) {
-            uint32_t v[3][4];
-#pragma unroll
-            for (int i = 0; i < 3; ++i) tmem_ld4(base + i * RP + c0, v[i]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c0 + e < r)
-                    sink(c0 + e, __uint_as_float(v[0][e]) + (__uint_as_float(v[1][e]) + __uint_as_float(v[2][e])));
-        }
-    } else {
-        for (int c0 = 0; c0 < RP; c0 += 16) {
-            uint32_t hi[16], lo[16];
-            tmem_ld16(base + c0, hi);
-            tmem_ld16(base + RP + c0, lo);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (c0 + e < r) sink(c0 + e, __uint_as_float(hi[e]) + __uint_as_float(lo[e]));
-        }
-    }
-}
-
-template <bool kG, bool kD, bool kOnes, int NT>
+template <bool kG, bool kD, bool kOnes>
 __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_constant__ CUtensorMap tmT,
                                                               int t3d, RankTcArgs a, int* status) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const RtLayout L(Parts{kG, kD, kOnes}, a.r, kD && a.vbulk, NT);
+    const RtLayout L(Parts{kG, kD, kOnes}, a.r, kD && a.vbulk);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bar);
     uint64_t* full = bars;        // [2] tile landed
     uint64_t* vready = bars + 2;  // [2] Vcat table written
@@ -188,10 +135,7 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
     uint64_t* dfull = bars + 10;  // column accumulator final
     uint64_t* rbar = bars + 11;   // every CTA of the cluster delivered this CTA's column slice
     uint64_t* vfull = bars + 12;  // [2] vbulk: the tile's V rows landed
-    uint64_t* dgroup = bars + 14;  // [2] NT = 3: a group's column sums are complete
-    uint64_t* dempty = bars + 16;  // [2] NT = 3: and have been read
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
-    float* drained = reinterpret_cast<float*>(smem + L.drain);  // NT = 3
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
     // recv[q][c][j]: partial of CTA q for column cbeg + c of this CTA's slice
     float* recv = reinterpret_cast<float*>(smem + L.recv);
 
@@ -221,8 +165,6 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
             mbar_init(&gfull[s], 1);
             mbar_init(&gempty[s], kWorkers);
             mbar_init(&vfull[s], 1);
-            mbar_init(&dgroup[s], 1);
-            mbar_init(&dempty[s], kWorkers);
         }
         mbar_init(dfull, 1);
         mbar_init(rbar, static_cast<uint32_t>(CL * (cend > cbeg ? cend - cbeg : 1)));
@@ -305,22 +247,13 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
                 }
                 if constexpr (kD) {
                     // column sums: T^T (MN-major, the two blocks 64 columns apart) x Vcat
-                    const int grp = i / kDrain;
-                    const uint32_t dcol = L.d_col + (NT == 3 ? (grp & 1) * L.NV : 0);
-                    const bool fresh = NT == 3 ? i % kDrain == 0 : i == 0;
-                    if (NT == 3 && fresh && grp >= 2 && !mbar_wait(&dempty[grp & 1], ((grp >> 1) - 1) & 1, status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kTileRows / 16; ++kk) {
                         const uint64_t ad = smem_desc(tb + kk * 2048, kBoxBytes, 1024, kLayoutSw128);
                         const uint64_t bd =
                             smem_desc(vt + s * L.NV * 256 + kk * 256, 128, kTabSbo, kLayoutNone);
-                        mma_bf16(tmem + dcol, ad, bd, id_d, (!fresh || kk > 0) ? 1u : 0u);
+                        mma_bf16(tmem + L.d_col, ad, bd, id_d, (i > 0 || kk > 0) ? 1u : 0u);
                     }
-                    if (NT == 3 && (i % kDrain == kDrain - 1 || i == nt - 1)) mma_commit(&dgroup[grp & 1]);
                 }
                 mma_commit(&empty[s]);
             }
@@ -351,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (j0 + e < L.RP) put_split<NT>(bt, j0 + e, L.RP, rr, (j0 + e < a.r && n < a.C) ? v[e] : 0.f);
+                    put_split(bt, j0 + e, L.RP + j0 + e, rr, (j0 + e < a.r && n < a.C) ? v[e] : 0.f);
             }
             if constexpr (!kD) {
                 // G alone: the MMAs of the first tile wait for this table on vready[0]
@@ -368,30 +301,20 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
             const int m = (t0 + i) * kTileRows + rr;
             const uint32_t base = tmem + lane_base + L.g_col + b * L.NG;
             float* g = a.Gp + (static_cast<size_t>(cb) * a.M + m) * a.r;
-            read_sums<NT>(base, L.RP, a.r, [&](int j, float sum) {
-                if (m < a.M) g[j] = sum;
-            });
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&gempty[b]);
-        };
-        // NT = 3: adds group g's column sums to this column's running ones
-        auto drain_group = [&](int g) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&dgroup[g & 1], (g >> 1) & 1, status));
-            if (!ok) return;
-            tc_fence_after();
-            const uint32_t base = tmem + lane_base + L.d_col + (g & 1) * L.NV;
-            float* row = drained + rr * L.JP;
-            read_sums<NT>(base, L.RP, a.r, [&](int j, float sum) { row[j] = g == 0 ? sum : row[j] + sum; });
-            if constexpr (kOnes) {
-                uint32_t ones[4];
-                tmem_ld4(base + NT * L.RP, ones);
+            for (int c0 = 0; c0 < L.RP; c0 += 16) {
+                uint32_t hi[16], lo[16];
+                tmem_ld16(base + c0, hi);
+                tmem_ld16(base + L.RP + c0, lo);
                 tmem_ld_wait();
-                row[a.r] = g == 0 ? __uint_as_float(ones[0]) : row[a.r] + __uint_as_float(ones[0]);
+                if (m < a.M) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (c0 + e < a.r) g[c0 + e] = __uint_as_float(hi[e]) + __uint_as_float(lo[e]);
+                }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&dempty[g & 1]);
+            if (lane == 0) mbar_arrive(&gempty[b]);
         };
         if constexpr (kG && !kD) {
             // the Bcat table is the only operand the workers write
@@ -403,16 +326,16 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
             const int tw = threadIdx.x - 64;  // 0 .. 127
             if (a.vbulk) {
                 // the parts of both V tables that no tile changes: zero rows
-                // beyond r in the terms' parts, and the ones block
+                // beyond r in the head and remainder halves, and the ones block
                 // (a ones row, then zeros; the tile's rows past M are zero, so
                 // their ones add nothing), as 16-byte chunks of 8 tile rows
-                const int nconst = L.NV - NT * a.r;
+                const int nconst = L.NV - 2 * a.r;
                 for (int idx = tw; idx < 2 * nconst * 16; idx += 32 * kWorkers) {
                     const int b = idx / (nconst * 16), rem = idx % (nconst * 16);
                     const int jj = rem / 16, kg = rem % 16;
-                    const int pad = L.RP - a.r;  // zero rows of one term
-                    const int j = jj < NT * pad ? jj / pad * L.RP + a.r + jj % pad : NT * L.RP + jj - NT * pad;
-                    const uint32_t w = (kOnes && j == NT * L.RP) ? 0x3F803F80u : 0u;  // bf16 1.0 pairs
+                    const int j = jj < L.RP - a.r ? a.r + jj : (jj < 2 * (L.RP - a.r) ? L.RP + a.r + jj - (L.RP - a.r)
+                                                                                      : 2 * L.RP + jj - 2 * (L.RP - a.r));
+                    const uint32_t w = (kOnes && j == 2 * L.RP) ? 0x3F803F80u : 0u;  // bf16 1.0 pairs
                     *reinterpret_cast<uint4*>(smem + L.vtab + b * L.NV * 256 + ktab_off(j, 8 * kg)) =
                         make_uint4(w, w, w, w);
                 }
@@ -434,7 +357,7 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
                     const int mt0 = (t0 + i) * kTileRows;
                     for (int idx = tw; idx < a.r * 16; idx += 32 * kWorkers) {
                         const int kg = idx / a.r, j = idx % a.r;
-                        uint32_t w[NT][4];
+                        uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int e2 = 0; e2 < 4; ++e2) {
                             float v2[2];
@@ -443,18 +366,17 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
                                 const int row = 8 * kg + 2 * e2 + h;
                                 v2[h] = mt0 + row < a.M ? vr[row * a.r + j] : 0.f;
                             }
-                            __nv_bfloat16 t0[NT], t1[NT];
-                            split_terms<NT>(v2[0], t0);
-                            split_terms<NT>(v2[1], t1);
-#pragma unroll
-                            for (int i2 = 0; i2 < NT; ++i2)
-                                w[i2][e2] = static_cast<uint32_t>(__bfloat16_as_ushort(t0[i2])) |
-                                            (static_cast<uint32_t>(__bfloat16_as_ushort(t1[i2])) << 16);
+                            const __nv_bfloat16 h0 = __float2bfloat16_rn(v2[0]), h1 = __float2bfloat16_rn(v2[1]);
+                            const __nv_bfloat16 l0 = __float2bfloat16_rn(v2[0] - __bfloat162float(h0));
+                            const __nv_bfloat16 l1 = __float2bfloat16_rn(v2[1] - __bfloat162float(h1));
+                            hi[e2] = static_cast<uint32_t>(__bfloat16_as_ushort(h0)) |
+                                     (static_cast<uint32_t>(__bfloat16_as_ushort(h1)) << 16);
+                            lo[e2] = static_cast<uint32_t>(__bfloat16_as_ushort(l0)) |
+                                     (static_cast<uint32_t>(__bfloat16_as_ushort(l1)) << 16);
                         }
-#pragma unroll
-                        for (int i2 = 0; i2 < NT; ++i2)
-                            *reinterpret_cast<uint4*>(vt + ktab_off(i2 * L.RP + j, 8 * kg)) =
-                                make_uint4(w[i2][0], w[i2][1], w[i2][2], w[i2][3]);
+                        *reinterpret_cast<uint4*>(vt + ktab_off(j, 8 * kg)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(vt + ktab_off(L.RP + j, 8 * kg)) =
+                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 } else {
                 for (int j0 = 0; j0 < L.RP; j0 += 8) {
@@ -500,14 +422,13 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
                             for (int e = 0; e < nv; ++e) v[e] += __ldg(p + b * stride + e);
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (j0 + e < L.RP) put_split<NT>(vt, j0 + e, L.RP, rr, v[e]);
+                    for (int e = 0; e < 8; ++e) put_split(vt, j0 + e, L.RP + j0 + e, rr, v[e]);
                 }
                 if constexpr (kOnes) {
                     const __nv_bfloat16 one = __float2bfloat16_rn(mok ? 1.f : 0.f);
                     const __nv_bfloat16 zero = __float2bfloat16_rn(0.f);
-                    *reinterpret_cast<__nv_bfloat16*>(vt + ktab_off(NT * L.RP, rr)) = one;
-                    for (int j = NT * L.RP + 1; j < L.NV; ++j)
+                    *reinterpret_cast<__nv_bfloat16*>(vt + ktab_off(2 * L.RP, rr)) = one;
+                    for (int j = 2 * L.RP + 1; j < L.NV; ++j)
                         *reinterpret_cast<__nv_bfloat16*>(vt + ktab_off(j, rr)) = zero;
                 }
                 }
@@ -517,15 +438,9 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
                 if constexpr (kG) {
                     if (i >= 1) g_epilogue(i - 1);
                 }
-                if constexpr (NT == 3) {
-                    if (ok && i >= kDrain && i % kDrain == 0) drain_group(i / kDrain - 1);
-                }
             }
             if constexpr (kG) {
                 if (ok && nt >= 1) g_epilogue(nt - 1);
-            }
-            if constexpr (NT == 3) {
-                if (ok && nt >= 1) drain_group((nt - 1) / kDrain);
             }
             // this CTA's partial of column rr goes to the CTA that owns the column
             cluster_wait();  // every CTA of the cluster has initialised its barriers
@@ -533,15 +448,22 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
             const uint32_t dst = dsmem_addr(recv + (static_cast<int>(crank) * per + rr - owner * per) * L.JP,
                                             static_cast<uint32_t>(owner));
             if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(dfull, 0, status));
-            if (NT == 3 && ok && nt > 0) {
-                for (int j = 0; j < L.JP; ++j) dsmem_st(dst + 4 * j, drained[rr * L.JP + j]);
-            } else if (ok && nt > 0) {
+            if (ok && nt > 0) {
                 tc_fence_after();
                 const uint32_t base = tmem + lane_base + L.d_col;
-                read_sums<NT>(base, L.RP, a.r, [&](int j, float sum) { dsmem_st(dst + 4 * j, sum); });
+                for (int c0 = 0; c0 < L.RP; c0 += 16) {
+                    uint32_t hi[16], lo[16];
+                    tmem_ld16(base + c0, hi);
+                    tmem_ld16(base + L.RP + c0, lo);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (c0 + e < a.r)
+                            dsmem_st(dst + 4 * (c0 + e), __uint_as_float(hi[e]) + __uint_as_float(lo[e]));
+                }
                 if constexpr (kOnes) {
                     uint32_t ones[16];
-                    tmem_ld16(base + NT * L.RP, ones);
+                    tmem_ld16(base + 2 * L.RP, ones);
                     tmem_ld_wait();
                     dsmem_st(dst + 4 * a.r, __uint_as_float(ones[0]));
                 }
@@ -591,7 +513,7 @@ __global__ void __launch_bounds__(kThreads) k4_rank_tc_kernel(const __grid_const
     }
 }
 
-template <bool kG, bool kD, bool kOnes, int NT>
+template <bool kG, bool kD, bool kOnes>
 cudaError_t launch_tc(const void* T, RankTcArgs a, int* status, cudaStream_t s) {
     // T as [row][64-column block][64] when its rows split into whole blocks
     // (one box per tile), else one 2-D box per 64-column block
@@ -608,10 +530,10 @@ cudaError_t launch_tc(const void* T, RankTcArgs a, int* status, cudaStream_t s) 
                (reinterpret_cast<uintptr_t>(a.V) & 15) == 0)
                   ? 1
                   : 0;
-    const RtLayout L(Parts{kG, kD, kOnes}, a.r, kD && a.vbulk, NT);
-    if (L.tmem_cols > 512) return cudaErrorInvalidValue;  // never reached for r <= 64 (NT = 3: r <= 32)
+    const RtLayout L(Parts{kG, kD, kOnes}, a.r, kD && a.vbulk);
+    if (L.tmem_cols > 512) return cudaErrorInvalidValue;  // never reached for r <= 64
     const size_t smem = L.total + 1024;
-    auto kern = k4_rank_tc_kernel<kG, kD, kOnes, NT>;
+    auto kern = k4_rank_tc_kernel<kG, kD, kOnes>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const int mtiles = (a.M + kTileRows - 1) / kTileRows;
@@ -647,7 +569,7 @@ int rank_tc_col_blocks(int C) { return (C + kTileCols - 1) / kTileCols; }
 
 cudaError_t launch_rank_dy_tc(const void* dY, const float* B, const float* xA, int M, int N, int r,
                               float c, float* Gp, float* dB, float* dbias, int* status,
-                              cudaStream_t s, bool precise) {
+                              cudaStream_t s) {
     RankTcArgs a{};
     a.V = xA;
     a.nsl = 1;
@@ -659,10 +581,9 @@ cudaError_t launch_rank_dy_tc(const void* dY, const float* B, const float* xA, i
     a.C = N;
     a.r = r;
     a.c = c;
-    if (Gp && dB && precise && r <= kMaxPreciseR) return launch_tc<true, true, true, 3>(dY, a, status, s);
-    if (Gp && dB) return launch_tc<true, true, true, 2>(dY, a, status, s);
-    if (Gp) return launch_tc<true, false, false, 2>(dY, a, status, s);
-    if (dB) return launch_tc<false, true, true, 2>(dY, a, status, s);
+    if (Gp && dB) return launch_tc<true, true, true>(dY, a, status, s);
+    if (Gp) return launch_tc<true, false, false>(dY, a, status, s);
+    if (dB) return launch_tc<false, true, true>(dY, a, status, s);
     return cudaSuccess;
 }
 
@@ -676,7 +597,7 @@ cudaError_t launch_rank_x_tc(const void* X, const float* G, int nsl, int M, int 
     a.C = K;
     a.r = r;
     a.c = c;
-    return launch_tc<false, true, false, 2>(X, a, status, s);
+    return launch_tc<false, true, false>(X, a, status, s);
 }
 
 }  // namespace qlora

@@ -57,21 +57,6 @@ __device__ __forceinline__ void store_block(uint8_t* stg, const float (&v)[kEpiC
                 make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
     __syncwarp();
-    if (!vec) {
-        // rows of any alignment: element by element, 16 neighbouring lanes
-        // along a row (four elements of 8 rows at a time touched eight times
-        // the sectors)
-#pragma unroll
-        for (int it = 0; it < 16; ++it) {
-            const int rr = 2 * it + (lane >> 4), cc = lane & 15;
-            const int gr = row0 + rr, gn = n + cc;
-            if (gr < M && gr >= row_min && gn < N)
-                out[static_cast<size_t>(gr) * ldo + gn] =
-                    *reinterpret_cast<const OutT*>(stg + rr * P + cc * static_cast<int>(sizeof(OutT)));
-        }
-        __syncwarp();
-        return;
-    }
     constexpr int kChunks = kEpiCols * static_cast<int>(sizeof(OutT)) / 16;  // per row
     constexpr int kRowsPerIt = 32 / kChunks;
     constexpr int kElems = 16 / static_cast<int>(sizeof(OutT));              // per chunk
@@ -84,7 +69,7 @@ __device__ __forceinline__ void store_block(uint8_t* stg, const float (&v)[kEpiC
         if (gr < M && gr >= row_min && gn < N) {
             const uint4 val = *reinterpret_cast<const uint4*>(stg + rr * P + ch * 16);
             OutT* dst = out + static_cast<size_t>(gr) * ldo + gn;
-            if (gn + kElems <= N) {
+            if (vec && gn + kElems <= N) {
                 *reinterpret_cast<uint4*>(dst) = val;
             } else {
                 const OutT* e = reinterpret_cast<const OutT*>(&val);
@@ -92,6 +77,39 @@ __device__ __forceinline__ void store_block(uint8_t* stg, const float (&v)[kEpiC
                     if (gn + i < N) dst[i] = e[i];
             }
         }
+    }
+    __syncwarp();
+}
+
+// store_block for rows of any alignment: element by element, 16 neighbouring
+// lanes along a row (store_block's element-wise copies, four elements of 8 rows
+// at a time, touch eight times the sectors; for 10-column outputs, though, its
+// skipped chunks make it the faster).
+template <typename OutT>
+__device__ __forceinline__ void store_block_any(uint8_t* stg, const float (&v)[kEpiCols], int lane,
+                                                OutT* __restrict__ out, size_t ldo, int row0, int M, int n, int N,
+                                                int row_min = 0) {
+    constexpr int P = stage_pitch<OutT>();
+    uint4* my = reinterpret_cast<uint4*>(stg + lane * P);
+#pragma unroll
+    for (int i = 0; i < kEpiCols * static_cast<int>(sizeof(OutT)) / 16; ++i) {
+        if constexpr (sizeof(OutT) == 2)
+            my[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1], (__nv_bfloat16*)nullptr),
+                               pack2(v[8 * i + 2], v[8 * i + 3], (__nv_bfloat16*)nullptr),
+                               pack2(v[8 * i + 4], v[8 * i + 5], (__nv_bfloat16*)nullptr),
+                               pack2(v[8 * i + 6], v[8 * i + 7], (__nv_bfloat16*)nullptr));
+        else
+            my[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                               __float_as_uint(v[4 * i + 3]));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int it = 0; it < 16; ++it) {
+        const int rr = 2 * it + (lane >> 4), cc = lane & 15;
+        const int gr = row0 + rr, gn = n + cc;
+        if (gr < M && gr >= row_min && gn < N)
+            out[static_cast<size_t>(gr) * ldo + gn] =
+                *reinterpret_cast<const OutT*>(stg + rr * P + cc * static_cast<int>(sizeof(OutT)));
     }
     __syncwarp();
 }
