@@ -210,8 +210,6 @@ __global__ void __launch_bounds__(kRowsThreads) k1_rows_kernel(const __nv_bfloat
                 x[q][i] = (g * R + q < M && (FULL || c < nch)) ? p[c] : make_uint4(0u, 0u, 0u, 0u);
             }
         }
-        __syncwarp();
-        if (g + step < groups) fetch(g + step);
         float inv[R];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
@@ -228,6 +226,12 @@ __global__ void __launch_bounds__(kRowsThreads) k1_rows_kernel(const __nv_bfloat
             inv[q] = amax > 0.f ? __fdiv_rn(127.0f, amax) : 0.f;
             if (lane == 0 && g * R + q < M) sx[g * R + q] = __fdiv_rn(amax, 127.0f);
         }
+        // The next copy overwrites the rows that the loads above read: the loads
+        // must be complete, not only issued (behind other warps' loads they can
+        // wait longer than a copy from L2 takes), which the proxy fence orders.
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (g + step < groups) fetch(g + step);
         unsigned long long acc[R][RP];  // even and odd k apart
 #pragma unroll
         for (int q = 0; q < R; ++q)

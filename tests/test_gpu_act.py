@@ -61,6 +61,8 @@ FORWARD = [
     (1, 2048, 1000, 4), (1, 16, 1, 1), (7, 784, 130, 3), (16, 4096, 512, 4), (17, 96, 33, 8), (64, 528, 257, 16),
     (65, 784, 128, 4), (100, 4096, 128, 8), (130, 2048, 200, 16), (333, 784, 1001, 8), (300, 272, 96, 20),
     (128, 144, 40, 64), (250, 4112, 70, 4), (513, 1040, 3000, 4), (2048, 272, 2600, 4), (2050, 512, 2568, 16), (1600, 256, 3333, 8),
+    (2048, 2064, 2560, 4), (2048, 2064, 2576, 8), (9000, 2048, 264, 4), (9000, 1920, 40, 8), (5000, 4096, 24, 4),
+    (5000, 3600, 24, 8),
 ]
 
 
@@ -68,6 +70,26 @@ FORWARD = [
 @pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
 def test_forward_shapes(M, K, N, r, dt):
     run_forward(M, K, N, r, dt, "gelu_tanh", True, True, seed=M + N)
+
+
+@pytest.mark.parametrize("M,K,r", [(9000, 2048, 4), (9000, 2048, 8), (18000, 1000 // 16 * 16, 4), (5000, 4096, 4)])
+def test_input_codes_of_many_rows_are_the_same_every_time(M, K, r):
+    """The row quantizer's copies run ahead of the loads they replace: cold and
+    warm, alone and beside traffic, the codes are the definition's."""
+    L = make_layer(K, 16, r, BF16, _gen(M))
+    X = torch.randn(M, K, device="cuda").to(BF16)
+    q, sx = ref.row_codes(X)
+    trash = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    for i in range(40):
+        if i % 4 == 0:
+            trash.zero_()  # out of L2
+        if i % 4 == 1:
+            with torch.cuda.stream(side):
+                trash.zero_()
+        _, keep = qlora.forward_act(L, X, act="relu")
+        assert torch.equal(keep.Xq, q) and torch.equal(keep.sx, sx), i
+    torch.cuda.synchronize()
 
 
 @pytest.mark.parametrize("name", ["none", "relu", "gelu", "gelu_tanh", "silu"])
@@ -104,7 +126,7 @@ def run_backward(M, K, N, r, dt, name, add, seed=0, z=None, dY=None, want_dx=Tru
 BACKWARD = [
     (1, 16, 8, 1), (1, 2048, 512, 4), (16, 1024, 2048, 4), (17, 784, 136, 3), (64, 528, 264, 16), (65, 784, 128, 4),
     (127, 48, 64, 8), (129, 272, 200, 16), (333, 784, 1000, 8), (300, 272, 96, 20), (140, 144, 40, 33),
-    (256, 144, 72, 64), (77, 160, 10, 4), (202, 80, 12608, 4), (256, 48, 2048, 16), (70, 2048, 1032, 8), (1024, 2576, 128, 4), (1030, 2560, 192, 16), (2500, 528, 320, 8),
+    (256, 144, 72, 64), (77, 160, 10, 4), (202, 80, 12608, 4), (256, 48, 2048, 16), (70, 2048, 1032, 8), (1024, 2576, 128, 4), (1030, 2560, 192, 16), (2500, 528, 320, 8), (1100, 1280, 136, 4), (2100, 1040, 2056, 2),
 ]
 
 
@@ -144,7 +166,8 @@ def _pack_int4(codes):
 
 
 @pytest.mark.parametrize("M,K,N,r,dt", [(5, 256, 160, 4, BF16), (200, 288, 161, 8, BF16), (150, 96, 72, 4, F32),
-                                        (2100, 256, 2568, 4, BF16), (2100, 256, 2565, 16, BF16)])
+                                        (2100, 256, 2568, 4, BF16), (2100, 256, 2565, 16, BF16),
+                                        (1100, 1280, 136, 4, BF16)])
 def test_int4_kernels_match_their_int8_codes(M, K, N, r, dt):
     """Packed int4 codes give what the same codes give as int8: to the last bit
     on the same kernel form, to half a step where the forms differ."""
@@ -402,10 +425,11 @@ def test_refusals_of_the_binding():
         qlora.ckpt_load(torch.zeros(8, 64, dtype=torch.int8, device="cuda"), torch.zeros(3, 8, device="cuda"))
 
 
-def test_streams_and_two_calls_at_once():
+@pytest.mark.parametrize("size", [(700, 272, 320), (2048, 1040, 2576)])
+def test_streams_and_two_calls_at_once(size):
     """Calls on two side streams with workspaces of their own, and outputs
     allocated on the stream that writes them."""
-    M, K, N, r = 700, 272, 320, 4
+    M, K, N, r = size + (4,)
     L = make_layer(K, N, r, BF16, _gen(5))
     X = torch.randn(M, K, device="cuda").to(BF16)
     dY = torch.randn(M, N, device="cuda").to(BF16)
@@ -519,18 +543,20 @@ def test_feed_forward_block(M, K, N, r, dt, name, skip):
     assert ff.kept_bytes() < 0.6 * M * (2 * K + 4 * N) * (ff.X.element_size() / 2) + M * 8 * (r + 2)
 
 
-@pytest.mark.parametrize("M,dt", [(48, BF16), (300, F32), (1100, BF16)])
-def test_captured_blocks_replay_on_new_inputs(M, dt):
+@pytest.mark.parametrize("M,K,N,dt", [(48, 64, 160, BF16), (300, 64, 160, F32), (1100, 64, 160, BF16),
+                                      (2048, 1040, 2576, BF16)])
+def test_captured_blocks_replay_on_new_inputs(M, K, N, dt):
     """Two captured blocks (each with its own workspace) replayed in turn and
     overlapping, on inputs that they were not captured with, give what eager
-    steps give, bit for bit."""
-    blocks = [make_block(M, 64, 160, 4, dt, "silu", seed=s) for s in (1, 2)]
+    steps give, bit for bit.  The largest takes the second stream and the
+    de-quantized kernel."""
+    blocks = [make_block(M, K, N, 4, dt, "silu", seed=s) for s in (1, 2)]
     for b in blocks:
         b.capture()
     for rep in range(3):
         for i, b in enumerate(blocks):
-            b.X.copy_(torch.randn(M, 64, generator=_gen(10 * rep + i), device="cuda").to(dt))
-            b.dY.copy_(torch.randn(M, 64, generator=_gen(99 + rep + i), device="cuda").to(dt))
+            b.X.copy_(torch.randn(M, K, generator=_gen(10 * rep + i), device="cuda").to(dt))
+            b.dY.copy_(torch.randn(M, K, generator=_gen(99 + rep + i), device="cuda").to(dt))
         torch.cuda.synchronize()
         streams = [torch.cuda.Stream() for _ in blocks]
         for b, s in zip(blocks, streams):
