@@ -448,7 +448,8 @@ typedef enum {
 /* Epilogue of a forward GEMM (host struct of device pointers).  residual
  * [M,N] act_dtype, 16-byte aligned, or NULL; it may be Y itself (in place).
  * zq [M,N] int8 (16-byte aligned) and zs [ceil(N/32)][M] fp32 receive the 8-bit
- * checkpoint of Z; both, or both NULL. */
+ * checkpoint of Z; both, or both NULL.  Neither Y nor zq may be Xq.  At most
+ * 2^30 rows. */
 typedef struct {
     qlora_activation act;
     const void* residual;
@@ -458,7 +459,8 @@ typedef struct {
 
 /* Epilogue of a dX GEMM.  zq [M,K] (16-byte aligned) and zs [ceil(K/32)][M]:
  * the checkpoint of the z whose activation is X; read unless act is NONE.
- * add [M,K] act_dtype, 16-byte aligned, or NULL; it may be dX itself. */
+ * add [M,K] act_dtype, 16-byte aligned, or NULL; it may be dX itself.  dX may
+ * be neither dY, zq nor Xq.  At most 4194240 rows. */
 typedef struct {
     qlora_activation act;
     const int8_t* zq;
@@ -534,7 +536,7 @@ int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, cons
 
 /* T [rows, cols] (dtype; 16-byte aligned) -> its 8-bit checkpoint q [rows, cols]
  * (16-byte aligned), scales [ceil(cols/32)][rows].  Bit-exact with the reading
- * above.  rows == 0 is a no-op. */
+ * above.  rows == 0 is a no-op; at most 2^30 rows and columns. */
 int qlora_ckpt_save(const void* T, int rows, int cols, qlora_dtype dtype, int8_t* q, float* scales, void* stream);
 
 /* T = q * scale, the product rounded to fp32 and then to `dtype`.  block 32:

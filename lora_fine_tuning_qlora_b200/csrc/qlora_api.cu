@@ -317,8 +317,13 @@ int qlora_quantize_input(const qlora_layer_desc* d, int M, const void* X, const 
                        "input quantizer launch");
 }
 
+// Row counts and block counts of the kernels are ints.
+constexpr int kMaxRows = 1 << 30;
+// Rows of qlora_gemm_dx_act: 65535 blocks of 64.
+constexpr int kMaxDxRows = 65535 * 64;
+
 // The checks of a forward epilogue and its part of the launch arguments.
-static int forward_epilogue(const qlora_fwd_epilogue* x, const void* Y, FwdEpilogue& ep) {
+static int forward_epilogue(const qlora_fwd_epilogue* x, int M, const int8_t* Xq, const void* Y, FwdEpilogue& ep) {
     if (!x) return QLORA_OK;
     QL_REQUIRE(x->act >= QLORA_ACT_NONE && x->act <= QLORA_ACT_SILU, QLORA_EINVAL, "unknown activation");
     QL_REQUIRE((x->zq == nullptr) == (x->zs == nullptr), QLORA_EINVAL,
@@ -326,7 +331,10 @@ static int forward_epilogue(const qlora_fwd_epilogue* x, const void* Y, FwdEpilo
     QL_REQUIRE(!x->residual || aligned(x->residual, 16), QLORA_EALIGN, "residual must be 16-byte aligned");
     QL_REQUIRE(!x->zq || (aligned(x->zq, 16) && aligned(x->zs, 4)), QLORA_EALIGN,
                "zq must be 16-byte aligned, zs 4-byte aligned");
-    QL_REQUIRE(!x->zq || static_cast<const void*>(x->zq) != Y, QLORA_EINVAL, "zq must not alias Y");
+    QL_REQUIRE(!x->zq || (static_cast<const void*>(x->zq) != Y && x->zq != Xq), QLORA_EINVAL,
+               "zq must not alias Y or Xq");
+    QL_REQUIRE(static_cast<const void*>(Xq) != Y, QLORA_EINVAL, "Y must not alias Xq");
+    QL_REQUIRE(M <= kMaxRows, QLORA_ESHAPE, "more than 2^30 rows");
     ep.ex = x->act != QLORA_ACT_NONE || x->residual || x->zq;
     ep.act = static_cast<int>(x->act);
     ep.res = x->residual;
@@ -350,7 +358,7 @@ static int gemm_forward_impl(const qlora_layer_desc* d, int M, const int8_t* Xq,
                    (!bias || aligned(bias, 4)) && (!acc || aligned(acc, 4)),
                QLORA_EALIGN, "fp32/int32 vectors must be 4-byte aligned");
     FwdEpilogue ep;
-    rc = forward_epilogue(x, Y, ep);
+    rc = forward_epilogue(x, M, Xq, Y, ep);
     if (rc != QLORA_OK) return rc;
     if (M == 0) return QLORA_OK;
     int* status = status_ptr();
@@ -410,7 +418,7 @@ int qlora_forward_act(const qlora_layer_desc* d, int M, const void* X, const int
                    (!bias || aligned(bias, 4)),
                QLORA_EALIGN, "fp32 vectors must be 4-byte aligned");
     FwdEpilogue ep;
-    rc = forward_epilogue(epilogue, Y, ep);
+    rc = forward_epilogue(epilogue, M, Xq, Y, ep);
     if (rc != QLORA_OK) return rc;
     if (M == 0) return QLORA_OK;
     int* status = status_ptr();
@@ -524,7 +532,7 @@ static size_t ckpt_dense_offset(const qlora_layer_desc* d, int M) {
 }
 
 // The checks of a dX epilogue and its part of the launch arguments.
-static int dx_epilogue(const qlora_dx_epilogue* x, DxEpilogue& ep) {
+static int dx_epilogue(const qlora_dx_epilogue* x, int M, const void* dY, const void* dX, DxEpilogue& ep) {
     if (!x) return QLORA_OK;
     QL_REQUIRE(x->act >= QLORA_ACT_NONE && x->act <= QLORA_ACT_SILU, QLORA_EINVAL, "unknown activation");
     QL_REQUIRE(x->act == QLORA_ACT_NONE || (x->zq && x->zs), QLORA_EINVAL,
@@ -532,6 +540,9 @@ static int dx_epilogue(const qlora_dx_epilogue* x, DxEpilogue& ep) {
     QL_REQUIRE(x->act == QLORA_ACT_NONE || (aligned(x->zq, 16) && aligned(x->zs, 4)), QLORA_EALIGN,
                "zq must be 16-byte aligned, zs 4-byte aligned");
     QL_REQUIRE(!x->add || aligned(x->add, 16), QLORA_EALIGN, "add must be 16-byte aligned");
+    QL_REQUIRE(dX != dY, QLORA_EINVAL, "dX must not alias dY");
+    QL_REQUIRE(x->act == QLORA_ACT_NONE || dX != x->zq, QLORA_EINVAL, "dX must not alias zq");
+    QL_REQUIRE(M <= kMaxDxRows, QLORA_ESHAPE, "more than 4194240 rows");
     ep.ex = x->act != QLORA_ACT_NONE || x->add;
     ep.act = static_cast<int>(x->act);
     ep.zq = x->zq;
@@ -554,7 +565,7 @@ static int gemm_dx_impl(const qlora_layer_desc* d, int M, const void* dY, const 
     QL_REQUIRE(aligned(sw, 4) && aligned(A, 4), QLORA_EALIGN, "fp32 vectors must be 4-byte aligned");
     QL_REQUIRE(!gate || aligned(gate, 16), QLORA_EALIGN, "X must be 16-byte aligned");
     DxEpilogue ep;
-    rc = dx_epilogue(x, ep);
+    rc = dx_epilogue(x, M, dY, dX, ep);
     if (rc != QLORA_OK) return rc;
     if (M == 0) return QLORA_OK;
     const WsLayout w = layout_for(*d, M);
@@ -818,10 +829,11 @@ int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, cons
                    aligned(dA, 4) && aligned(dB, 4) && (!dbias || aligned(dbias, 4)),
                QLORA_EALIGN, "fp32 vectors must be 4-byte aligned");
     QL_REQUIRE(M <= kRankQMaxRows, QLORA_EUNSUPPORTED, "more than 1047552 rows would overflow the int32 sums");
-    DxEpilogue checked;
-    rc = dx_epilogue(epilogue, checked);
-    if (rc != QLORA_OK) return rc;
     const qlora_dx_epilogue none_or = epilogue ? *epilogue : qlora_dx_epilogue{QLORA_ACT_NONE, nullptr, nullptr, nullptr};
+    DxEpilogue checked;
+    rc = dx_epilogue(&none_or, M, dY, dX, checked);
+    if (rc != QLORA_OK) return rc;
+    QL_REQUIRE(!dX || static_cast<const void*>(Xq) != dX, QLORA_EINVAL, "dX must not alias Xq");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (M == 0) {
         rc = cuda_status(cudaMemsetAsync(dA, 0, sizeof(float) * d->K * d->r, s), "memset dA");
@@ -882,6 +894,7 @@ int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, cons
 
 static int check_ckpt(const void* T, int rows, int cols, qlora_dtype dtype, const void* q, const void* scales) {
     QL_REQUIRE(rows >= 0 && cols >= 1, QLORA_ESHAPE, "rows must be >= 0 and cols >= 1");
+    QL_REQUIRE(rows <= kMaxRows && cols <= kMaxRows, QLORA_ESHAPE, "more than 2^30 rows or columns");
     QL_REQUIRE(T && q && scales, QLORA_EINVAL, "NULL pointer argument");
     QL_REQUIRE(dtype == QLORA_F32 || dtype == QLORA_BF16, QLORA_EINVAL, "unknown activation dtype");
     QL_REQUIRE(aligned(T, 16) && aligned(q, 16) && aligned(scales, 4), QLORA_EALIGN,

@@ -101,6 +101,21 @@ def test_checkpoint_refusals(q):
     assert save(P, 0, 4, 0, P, P, None) == 0 and load(P, P, 0, 4, 32, 0, P, None) == 0
 
 
+def test_overlap_and_row_limit_refusals(q):
+    """Outputs over inputs that are still read, and row counts that would leave
+    the kernels' 32-bit block counts or the grid."""
+    assert forward_act(q, zq=3 * P, zs=P) == EINVAL and forward_act(q, Xq=2 * P) == EINVAL
+    assert forward_act(q, M=(1 << 30) + 1) == ESHAPE and gemm_act(q, M=2147483647) == ESHAPE
+    assert backward(q, act=2, zq=2 * P, zs=P) == EINVAL and backward(q, Xq=2 * P) == EINVAL
+    d = q.desc(64, 48, 4, 8.0, BF16)
+    e = ctypes.byref(q.DxEpilogue(0, None, None, None))
+    for M, dX, code in ((16, P, EINVAL), (4194241, 2 * P, ESHAPE)):
+        assert q.lib().qlora_gemm_dx_act(ctypes.byref(d), M, P, P, P, P, e, dX, P, 1 << 40, None) == code
+    for save in (q.lib().qlora_ckpt_save, lambda *a: q.lib().qlora_ckpt_load(a[0], a[4], a[1], a[2], 32, a[3], *a[5:])):
+        for rows, cols in ((2147483647, 1), (1, 2147483647)):
+            assert save(P, rows, cols, 0, P, P, None) == ESHAPE
+
+
 def test_sizes(q):
     lib = q.lib()
     assert lib.qlora_ckpt_scales(5, 32) == 5 and lib.qlora_ckpt_scales(5, 33) == 10
