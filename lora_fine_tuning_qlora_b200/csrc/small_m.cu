@@ -25,6 +25,10 @@
 // into the now idle operand ring), a second cluster barrier publishes them,
 // and CTA q adds the S partials in rank order (exact for int32, a fixed
 // order for fp32) and writes its columns.  Every wait is bounded.
+#include <map>
+#include <mutex>
+#include <tuple>
+
 #include "internal.h"
 #include "ptx.cuh"
 #include "dx_common.cuh"
@@ -36,8 +40,10 @@ namespace {
 
 constexpr int kCh = 128;                 // output channels per CTA (the MMA's M)
 constexpr int kRing = 192 * 1024;        // operand ring; later the partial-sum buffer
+constexpr int kHalfRing = 94 * 1024;     // two CTAs per SM
 constexpr int kTabFloats = 256 * 17;     // per owner column: the row's rank-r factor row and scale
-constexpr int kBarOff = kRing + kTabFloats * 4;  // barriers after the ring and the table
+constexpr int kTail = kTabFloats * 4 + 256 + 1024;  // the table, the barriers, the alignment
+static_assert(kHalfRing % 1024 == 0 && 2 * (kHalfRing + kTail + 1024) <= 233472, "two CTAs per SM");
 constexpr int kMaxStages = 8;
 constexpr int kEpiW = 4;                 // epilogue warps: one per TMEM lane quarter
 constexpr int kDqW = 8;                  // de-quantize warps (dX)
@@ -52,6 +58,7 @@ struct SmallArgs {
     int MP;               // tokens padded to a multiple of 16
     int S;                // split of the contraction (cluster size along y)
     int stages;           // ring depth
+    int ring;             // bytes of the ring
     int kblocks;          // contraction blocks in total
     uint32_t tmem_cols;
 };
@@ -61,7 +68,7 @@ __device__ __forceinline__ void cluster_sync_all() {
     cluster_wait();
 }
 
-// smem: [ring kRing][barriers]
+// smem: [ring][table][barriers]
 __device__ __forceinline__ uint8_t* aligned_smem(uint8_t* raw) {
     return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
 }
@@ -101,7 +108,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     SmallArgs a, FwdEpilogue ep, int* status) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = aligned_smem(smem_raw);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + a.ring + kTabFloats * 4);
     uint64_t* empty = full + kMaxStages;
     uint64_t* wready = empty + kMaxStages;  // W4: the int8 tile expanded
     uint64_t* accf = wready + kMaxStages;
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         {
             // the owner columns' xA rows and row scales, while the MMAs run
             const int Wo = a.MP / a.S;
-            float* tab = reinterpret_cast<float*>(smem + kRing);
+            float* tab = reinterpret_cast<float*>(smem + a.ring);
             const int t = threadIdx.x - 64;
             for (int e = t; e < Wo * (RMAX + 1); e += 32 * kEpiW) {
                 const int cl = e / (RMAX + 1), j = e % (RMAX + 1);
@@ -249,7 +256,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float swn = nok ? __ldg(ep.sw + n) : 0.f;
         const float bn = (nok && ep.bias) ? __ldg(ep.bias + n) : 0.f;
         OutT* Y = static_cast<OutT*>(ep.Y);
-        const float* tab = reinterpret_cast<const float*>(smem + kRing);
+        const float* tab = reinterpret_cast<const float*>(smem + a.ring);
         // EX: the residual of the next token is loaded a token ahead (it may
         // lie in Y's own buffer: read here before it is written)
         const OutT* res = EX ? static_cast<const OutT*>(ep.res) : nullptr;
@@ -313,7 +320,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
                     const float* __restrict__ sw, SmallArgs a, DxEpilogue ep, int* status) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = aligned_smem(smem_raw);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + a.ring + kTabFloats * 4);
     uint64_t* wready = full + kMaxStages;
     uint64_t* empty = wready + kMaxStages;
     uint64_t* accf = empty + kMaxStages;
@@ -463,7 +470,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
         {
             // the owner columns' G rows (c G), while the MMAs run
             const int Wo = a.MP / a.S;
-            float* tab = reinterpret_cast<float*>(smem + kRing);
+            float* tab = reinterpret_cast<float*>(smem + a.ring);
             const int t = threadIdx.x - 32 * (2 + kDqW);
             for (int e = t; e < Wo * RMAX; e += 32 * kEpiW) {
                 const int cl = e / RMAX, j = e % RMAX;
@@ -501,7 +508,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
         for (int j = 0; j < RMAX; ++j) aj[j] = (kok && j < ep.r) ? a_at(ep, k, j) : 0.f;
         __nv_bfloat16* dX = static_cast<__nv_bfloat16*>(ep.dX);
         const __nv_bfloat16* gate = static_cast<const __nv_bfloat16*>(ep.gate);
-        const float* tab = reinterpret_cast<const float*>(smem + kRing);
+        const float* tab = reinterpret_cast<const float*>(smem + a.ring);
         // EX: z and the added gradient of the next token, loaded a token ahead
         const __nv_bfloat16* add = EX ? static_cast<const __nv_bfloat16*>(ep.add) : nullptr;
         float znext = 0.f, anext = 0.f;
@@ -559,6 +566,65 @@ int pick_split(int tiles, int kblocks) {
     return s;
 }
 
+// Clusters of S CTAs (along y) that are resident at once, looked up once per
+// kernel, size and device.
+int resident_clusters(const void* kern, int threads, int S, int smem) {
+    static std::mutex mu;
+    static std::map<std::tuple<const void*, int, int, int>, int> seen;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_tuple(kern, S, smem, dev);
+    const auto it = seen.find(key);
+    if (it != seen.end()) return it->second;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, S);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = S;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+    }
+    return seen[key] = n;
+}
+
+// Ring, ring depth and, where `free_split` allows, the split.  A cluster lies
+// within one group of SMs, so fewer large ones are resident than the SM count
+// suggests (15 of eight whole-SM CTAs, not 18), and one more would run in a
+// second wave.  The forward's grids of up to twice as many take half the ring
+// and two CTAs per SM (two fit by shared memory, registers and TMEM columns;
+// the occupancy call does not count the second).  16 x 16384 x 2048 with its
+// input quantizer, cold: 34.8 us in two waves, 30.7 with half the split, 22.6
+// with half the ring.
+cudaError_t plan(const void* kern, int threads, int tiles, uint32_t stage, bool two_per_sm, bool free_split,
+                 SmallArgs& a) {
+    cudaError_t e = ensure_smem_attr(kern, kRing + kTail);
+    if (e != cudaSuccess) return e;
+    a.ring = kRing;
+    while (a.S >= 4) {
+        const int fit = resident_clusters(kern, threads, a.S, kRing + kTail);
+        if (tiles <= fit) break;
+        if (two_per_sm && tiles <= 2 * fit && a.MP * kCh * 4 <= kHalfRing &&
+            3 * static_cast<int>(stage) <= kHalfRing) {
+            a.ring = kHalfRing;
+            break;
+        }
+        if (!free_split) break;
+        a.S /= 2;
+    }
+    const int fit = a.ring / static_cast<int>(stage);
+    a.stages = fit > kMaxStages ? kMaxStages : fit;
+    return cudaSuccess;
+}
+
 }  // namespace
 
 bool small_m_applies(int M, int out_channels, int r, int contraction, bool ex) {
@@ -587,7 +653,6 @@ cudaError_t launch_gemm_i8_fwd_small(Act act, const int8_t* Xq, const int8_t* Wq
     const int tiles = (N + kCh - 1) / kCh;
     a.S = pick_split(tiles, a.kblocks);
     const uint32_t stage = kCh * 128 + static_cast<uint32_t>(a.MP) * 128 + (w4 ? kCh * 64 : 0);
-    a.stages = static_cast<int>(kRing / stage) > kMaxStages ? kMaxStages : static_cast<int>(kRing / stage);
     a.tmem_cols = pow2_cols(a.MP);
     CUtensorMap tw, tx;
     const bool wok = w4 ? make_tmap_2d(&tw, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, N, K / 2, K / 2, kCh, 64,
@@ -597,12 +662,11 @@ cudaError_t launch_gemm_i8_fwd_small(Act act, const int8_t* Xq, const int8_t* Wq
     if (!wok ||
         !make_tmap_2d(&tx, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, M, K, K, a.MP, 128, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    const size_t smem = kBarOff + 1024 + 256;
-    const dim3 grid(tiles, a.S);
     auto run = [&](auto kern) -> cudaError_t {
-        cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
+        // (integer sums: the split does not change them)
+        cudaError_t e = plan(reinterpret_cast<const void*>(kern), kFwdThreads, tiles, stage, true, true, a);
         if (e != cudaSuccess) return e;
-        return launch_k(kern, grid, dim3(kFwdThreads), smem, s, a.S, tw, tx, a, ep, status);
+        return launch_k(kern, dim3(tiles, a.S), dim3(kFwdThreads), a.ring + kTail, s, a.S, tw, tx, a, ep, status);
     };
     // by rank, then by codes and epilogue form
 #define QL_FWD_SMALL(T, R)                                                                          \
@@ -630,7 +694,6 @@ cudaError_t launch_gemm_dx_small(const void* dY, const int8_t* Wq, const float* 
     const int tiles = (K + kCh - 1) / kCh;
     a.S = pick_split(tiles, a.kblocks);
     const uint32_t stage = kDqTileBytes + kCodeBytes + static_cast<uint32_t>(a.MP) * 128;
-    a.stages = static_cast<int>(kRing / stage) > kMaxStages ? kMaxStages : static_cast<int>(kRing / stage);
     a.tmem_cols = pow2_cols(a.MP);
     CUtensorMap ty, tw;
     if (!make_tmap_2d(&ty, dY, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, M, N, static_cast<uint64_t>(N) * 2, a.MP,
@@ -640,12 +703,10 @@ cudaError_t launch_gemm_dx_small(const void* dY, const int8_t* Wq, const float* 
              : make_tmap_2d(&tw, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, N, K, K, 64, kCh,
                             CU_TENSOR_MAP_SWIZZLE_NONE)))
         return cudaErrorInvalidValue;
-    const size_t smem = kBarOff + 1024 + 256;
-    const dim3 grid(tiles, a.S);
     auto run = [&](auto kern) -> cudaError_t {
-        cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
+        cudaError_t e = plan(reinterpret_cast<const void*>(kern), kDxThreads, tiles, stage, false, ep.ex, a);
         if (e != cudaSuccess) return e;
-        return launch_k(kern, grid, dim3(kDxThreads), smem, s, a.S, ty, tw, sw, a, ep, status);
+        return launch_k(kern, dim3(tiles, a.S), dim3(kDxThreads), a.ring + kTail, s, a.S, ty, tw, sw, a, ep, status);
     };
 #define QL_DX_SMALL(R)                                                                    \
     (ep.ex ? (w4 ? run(k3_small_kernel<R, true, true>) : run(k3_small_kernel<R, false, true>)) \
