@@ -218,10 +218,14 @@ cudaError_t launch_rank_x_tc(const void* X, const float* G, int nsl, int M, int 
 // dA = c X^T G from the input kept as row codes, X = Xq sx (k4_rank_q.cu): sx G
 // as 8-bit digits in `digits` (rank_q_digit_bytes, 256-byte aligned), then the
 // column sums of Xq on the int8 tensor cores.  M at most kRankQMaxRows.
+// kDigits, kSum: one of the two steps (for up to 128 rows the second makes the
+// digits itself).
+enum class RankQPart { kBoth, kDigits, kSum };
 constexpr int kRankQMaxRows = 8 * 1023 * 128;
 size_t rank_q_digit_bytes(int M, int r);
 cudaError_t launch_rank_x_q(const int8_t* Xq, const float* sx, const float* G, int nsl, int M, int K, int r,
-                            float c, void* digits, float* dA, int* status, cudaStream_t s);
+                            float c, void* digits, float* dA, int* status, cudaStream_t s,
+                            RankQPart part_of = RankQPart::kBoth, bool early = false);
 
 // ---------------------------------------------------------------- 8-bit checkpoints
 // Blocks of 32 columns of a row: codes q [rows, cols], scales [ceil(cols/32)][rows] (ckpt.cu).

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(K3Cfg<MSUB, BN, RMAX>::kThreads, 1)
     const int num_k = (K + BN - 1) / BN;
     const int tiles = ((M + C::kBM - 1) / C::kBM) * num_k;
     const int nkb = (N + kBKn - 1) / kBKn;
-    pdl_trigger();
+    if constexpr (!EX) pdl_trigger();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(K3Cfg<MSUB, BN, RMAX>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();  // the prologue above touched no global memory
+    if constexpr (EX) pdl_trigger();  // after the wait: see launch_rank_x_q
 
     if (warp == 0) {
         // ------------------------------------------------------ producer

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int num_kt = (K + kPN - 1) / kPN;
     const int tiles = ((M + 2 * kPM - 1) / (2 * kPM)) * num_kt;
     const int nkb = (N + kPK - 1) / kPK;
-    pdl_trigger();
+    if constexpr (!EX) pdl_trigger();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     cluster_arrive();
     cluster_wait();
     pdl_wait();  // nothing above touched global memory
+    if constexpr (EX) pdl_trigger();  // after the wait: see launch_rank_x_q
 
     if (warp == 0) {
         // ------------------------------------------------------ producer

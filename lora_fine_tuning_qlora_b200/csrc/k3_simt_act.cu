@@ -36,8 +36,8 @@ __global__ void __launch_bounds__(kThreads) k3_simt_act_kernel(const T* __restri
     __shared__ float sD[2][kStep][kRows + 1];
     static_assert(sizeof(sD) >= kRows * 65 * sizeof(float), "c G rows of the tile");
     float(*sG)[65] = reinterpret_cast<float(*)[65]>(&sD[0][0][0]);  // after the products
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();  // after the wait: see launch_rank_x_q
     const int tid = threadIdx.x;
     const int tx = tid % 16, ty = tid / 16;
     const int split = static_cast<int>(blockIdx.x) % S;

@@ -162,6 +162,7 @@ struct RankQArgs {
     int M, K, r;
     int tiles_per_cta;
     int stages;
+    int early;              // wait for the predecessor at the end
     float c;
 };
 
@@ -179,6 +180,15 @@ struct RqLayout {
         while (tmem_cols < static_cast<uint32_t>(NV)) tmem_cols <<= 1;
     }
 };
+
+// sum_slices past L1: a kernel that has not waited for its predecessor must not
+// meet a line that the SM read before G was written.
+__device__ __forceinline__ float sum_slices_l2(const float* p, size_t stride, int n) {
+    float s = __ldcg(p);
+#pragma unroll 8
+    for (int b = 1; b < n; ++b) s += __ldcg(p + b * stride);
+    return s;
+}
 
 __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_constant__ CUtensorMap tmX, RankQArgs a,
                                                              int* status) {
@@ -230,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     cluster_arrive_relaxed();  // no CTA arrives on another's barrier before it is initialised
-    pdl_wait();
+    if (!a.early) pdl_wait();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -280,13 +290,23 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
             // the one tile's table (stage 0): thread = row
             const int m = threadIdx.x - 64;
             const size_t n = static_cast<size_t>(a.M) * a.r;
-            const float sxm = m < a.M ? __ldg(a.sx + m) : 0.f;
-            auto value = [&](int j) {
-                return m < a.M ? sum_slices(a.G + static_cast<size_t>(m) * a.r + j, n, a.nsl) * sxm : 0.f;
-            };
-            for (int j = 0; j < a.r; ++j) {
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(value(j)) & 0x7FFFFFFFu);
-                if (lane == 0) atomicMax(&s_top[j], top);
+            const float sxm = m < a.M ? __ldcg(a.sx + m) : 0.f;
+            float* sV = reinterpret_cast<float*>(smem + L.stage);  // [r][128], in the ring's idle second stage
+            for (int j0 = 0; j0 < a.r; j0 += 4) {
+                float v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    v[u] = 0.f;
+                    if (m < a.M && j0 + u < a.r)
+                        v[u] = sum_slices_l2(a.G + static_cast<size_t>(m) * a.r + j0 + u, n, a.nsl) * sxm;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (j0 + u >= a.r) break;
+                    sV[(j0 + u) * kRows + m] = v[u];
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v[u]) & 0x7FFFFFFFu);
+                    if (lane == 0) atomicMax(&s_top[j0 + u], top);
+                }
             }
             named_bar_sync(1, 128);
             if (m < 64) s_exp[m] = column_exponent(s_top[m]);
@@ -294,7 +314,7 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
             uint8_t* tab = smem + kTileBytes;
             for (int j = 0; j < L.RP; ++j) {
                 int d[4] = {0, 0, 0, 0};
-                if (j < a.r && s_exp[j] != kExpNaN) make_digits(value(j), s_exp[j], d);
+                if (j < a.r && s_exp[j] != kExpNaN) make_digits(sV[j * kRows + m], s_exp[j], d);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tab[digit_off(i * L.RP + j, m)] = static_cast<uint8_t>(d[i]);
             }
@@ -345,7 +365,6 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
     // touches this CTA's shared memory from outside
     const int width = cend - cbeg;
     if (width > 0 && mbar_wait_cluster(rbar, 0, status)) {
-        const int* pexp = own ? s_exp : reinterpret_cast<const int*>(a.digits);
         for (int idx = threadIdx.x; idx < width * a.r; idx += kThreads) {
             const int cc = idx / a.r, j = idx - cc * a.r;
             const int col = col0 + cbeg + cc;
@@ -353,12 +372,13 @@ __global__ void __launch_bounds__(kThreads) k4_rank_q_kernel(const __grid_consta
             long long sum = 0;
             for (int q = 0; q < static_cast<int>(CL); ++q)
                 sum += recv[static_cast<size_t>(q * per + cc) * a.r + j];
-            const int p = pexp[j];
+            const int p = own ? s_exp[j] : __ldcg(reinterpret_cast<const int*>(a.digits) + j);
             const double v = p == kExpNaN ? __longlong_as_double(0x7FF8000000000000LL)
                                           : scalbn(static_cast<double>(sum), -p) * static_cast<double>(a.c);
             a.dA[static_cast<size_t>(col) * a.r + j] = static_cast<float>(v);
         }
     }
+    if (a.early) pdl_wait();
 }
 
 }  // namespace
@@ -372,12 +392,18 @@ size_t rank_q_digit_bytes(int M, int r) {
     return digit_table_bytes(M, r) + kPrepCtas * 64 * 4 + static_cast<size_t>(M) * r * 4;
 }
 
+// `early`: the launch right before is a dX kernel that starts its dependents
+// only after its own pdl_wait(), so that everything before it, G and the
+// digits with it, is complete when this kernel starts.  It needs nothing of
+// that dX kernel: it runs beside it, on the SMs it leaves, and waits for it at
+// its end, so that whoever waits for this kernel has waited for both.
 cudaError_t launch_rank_x_q(const int8_t* Xq, const float* sx, const float* G, int nsl, int M, int K, int r,
-                            float c, void* digits, float* dA, int* status, cudaStream_t s) {
+                            float c, void* digits, float* dA, int* status, cudaStream_t s, RankQPart part_of,
+                            bool early) {
     if (M > kRankQMaxRows) return cudaErrorInvalidValue;
     const bool own = M <= kRows;
     cudaError_t e = cudaSuccess;
-    if (!own) {
+    if (!own && part_of != RankQPart::kSum) {
         uint8_t* buf = static_cast<uint8_t*>(digits);
         uint32_t* part = reinterpret_cast<uint32_t*>(buf + digit_table_bytes(M, r));
         float* V = reinterpret_cast<float*>(part + kPrepCtas * 64);
@@ -391,6 +417,7 @@ cudaError_t launch_rank_x_q(const int8_t* Xq, const float* sx, const float* G, i
                      s, 1, static_cast<const float*>(V), static_cast<const uint32_t*>(part), ctas, M, r, buf);
         if (e != cudaSuccess) return e;
     }
+    if (part_of == RankQPart::kDigits) return cudaSuccess;
     CUtensorMap tm;
     if (!make_tmap_2d(&tm, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, M, K, K, kRows, kCols, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
@@ -404,6 +431,7 @@ cudaError_t launch_rank_x_q(const int8_t* Xq, const float* sx, const float* G, i
     a.K = K;
     a.r = r;
     a.c = c;
+    a.early = early;
     const int mtiles = (M + kRows - 1) / kRows;
     a.tiles_per_cta = (mtiles + kMaxCl - 1) / kMaxCl;
     const int want = (rank_pass_rows() + kRows - 1) / kRows;  // a caller's minimum rows per CTA

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(PairActCfg<RP, FWD, W>::kThreads, 1)
         m0 = m0 * 2 * kTM + static_cast<int>(rank) * kTM;
         n0 *= kTN;
     };
-    pdl_trigger();
+    if constexpr (FWD) pdl_trigger();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(PairActCfg<RP, FWD, W>::kThreads, 1)
     cluster_arrive();
     cluster_wait();
     pdl_wait();  // nothing above touched global memory
+    if constexpr (!FWD) pdl_trigger();  // after the wait: see launch_rank_x_q
 
     if (warp == 0) {
         // ------------------------------------------------------ producer

@@ -788,14 +788,14 @@ size_t qlora_ckpt_workspace_bytes(const qlora_layer_desc* d, int M) {
 // Shared by the step-level call and the composite, both of which have
 // checked their arguments.
 static int grad_x_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, const float* sx, float* dA,
-                       void* workspace, cudaStream_t s) {
+                       void* workspace, cudaStream_t s, RankQPart part = RankQPart::kBoth, bool early = false) {
     const WsLayout w = layout_for(*d, M);
     int* status = status_ptr();
     QL_REQUIRE(status, QLORA_ECUDA, "no CUDA device");
     int nsl = 0;
     const float* g = g_source(w, workspace, &nsl);
     return cuda_status(launch_rank_x_q(Xq, sx, g, nsl, M, d->K, d->r, lora_scale(d),
-                                       static_cast<uint8_t*>(workspace) + w.total, dA, status, s),
+                                       static_cast<uint8_t*>(workspace) + w.total, dA, status, s, part, early),
                        "X pass launch");
 }
 
@@ -885,11 +885,15 @@ int qlora_backward_ckpt(const qlora_layer_desc* d, int M, const int8_t* Xq, cons
         if (rc_x != QLORA_OK) return rc_x;
         return rc_join2;
     }
-    if (dX) {
-        rc = gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, &none_or);
-        if (rc != QLORA_OK) return rc;
-    }
-    return grad_x_ckpt(d, M, Xq, sx, dA, workspace, s);
+    if (!dX) return grad_x_ckpt(d, M, Xq, sx, dA, workspace, s);
+    // One stream: the digits before the dX GEMM, the X pass behind it, beside
+    // its last CTAs (the kernels with an epilogue let it start early).
+    if (checked.ex) rc = grad_x_ckpt(d, M, Xq, sx, dA, workspace, s, RankQPart::kDigits);
+    if (rc != QLORA_OK) return rc;
+    rc = gemm_dx_impl(d, M, dY, Wq, sw, A, nullptr, dX, workspace, workspace_bytes, stream, false, &none_or);
+    if (rc != QLORA_OK) return rc;
+    return checked.ex ? grad_x_ckpt(d, M, Xq, sx, dA, workspace, s, RankQPart::kSum, true)
+                      : grad_x_ckpt(d, M, Xq, sx, dA, workspace, s);
 }
 
 static int check_ckpt(const void* T, int rows, int cols, qlora_dtype dtype, const void* q, const void* scales) {

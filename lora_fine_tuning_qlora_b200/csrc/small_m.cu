@@ -49,6 +49,7 @@ constexpr int kEpiW = 4;                 // epilogue warps: one per TMEM lane qu
 constexpr int kDqW = 8;                  // de-quantize warps (dX)
 constexpr int kFwdThreads = 32 * (2 + kEpiW);
 constexpr int kDxThreads = 32 * (2 + kDqW + kEpiW);
+constexpr int kMaxIssuers = 2;           // (forward, EX) MMA issuers: warp 1, then warps after the epilogue's
 constexpr int kMaxSplit = 8;
 constexpr int kMaxTokens = 64;           // above this the large-tile kernels measured as fast or faster
 constexpr int kMaxTokensEx = 256;        // (EX) ... unless their tiles are few: one MMA's N
@@ -61,6 +62,8 @@ struct SmallArgs {
     int ring;             // bytes of the ring
     int kblocks;          // contraction blocks in total
     uint32_t tmem_cols;
+    int issuers;          // (forward) MMA issuers, each with its own accumulator
+    int acc_cols;         // TMEM columns from one accumulator to the next
 };
 
 __device__ __forceinline__ void cluster_sync_all() {
@@ -78,13 +81,20 @@ __device__ __forceinline__ uint8_t* aligned_smem(uint8_t* raw) {
 // at the owner, the 32 rows of a warp in consecutive words (no bank
 // conflicts).  Warp q of the epilogue holds lane quarter q.
 __device__ __forceinline__ void send_partials(uint32_t tmem, int q, int lane, int MP, int W, uint32_t rank,
-                                              const uint32_t* recv_local) {
+                                              const uint32_t* recv_local, int accs, int acc_cols) {
     const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int row = q * 32 + lane;
     for (int c0 = 0; c0 < MP; c0 += 16) {
         uint32_t v[16];
         tmem_ld16(base + c0, v);
         tmem_ld_wait();
+        for (int i = 1; i < accs; ++i) {  // the issuers' accumulators (int32)
+            uint32_t u[16];
+            tmem_ld16(base + i * acc_cols + c0, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] += u[e];
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             const int c = c0 + e;
@@ -103,7 +113,7 @@ __device__ __forceinline__ void send_partials(uint32_t tmem, int q, int lane, in
 // EX: Y = act(Z) + res with Z kept in 8 bits (act_epilogue.cuh): a warp's 32
 // channels of a token are one block of the checkpoint.
 template <typename OutT, int RMAX, bool W4, bool EX>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(kFwdThreads + 32 * (EX ? kMaxIssuers - 1 : 0), 1)
     k2_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     SmallArgs a, FwdEpilogue ep, int* status) {
     extern __shared__ uint8_t smem_raw[];
@@ -130,7 +140,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_init(&empty[s], 1);
             mbar_init(&wready[s], kEpiW);
         }
-        mbar_init(accf, 1);
+        mbar_init(accf, a.issuers);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -160,10 +170,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 || (EX && warp >= 2 + kEpiW)) {
+        // issuer w takes blocks w, w + issuers, ...: the ring's depth is a
+        // multiple of the issuers, so a stage has one issuer for good (else an
+        // issuer could meet a stage two fills behind its parity)
+        const int w = EX && warp > 1 ? warp - (2 + kEpiW) + 1 : 0;
+        const int step = EX ? a.issuers : 1;
+        const uint32_t acc = tmem + static_cast<uint32_t>(w * a.acc_cols);
         if (lane == 0) {
             const uint32_t id = idesc_i8(128, a.MP);
-            for (int i = 0; i < nkb; ++i) {
+            for (int i = w; i < nkb; i += step) {
                 const int s = i % S;
                 if (!mbar_wait(&full[s], (i / S) & 1, status) ||
                     (W4 && !mbar_wait(&wready[s], (i / S) & 1, status)))
@@ -175,7 +191,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int kk = 0; kk < 4; ++kk) {
                     const uint64_t ad = smem_desc(wb + kk * 32, 16, 1024, kLayoutSw128);
                     const uint64_t bd = smem_desc(xb + kk * 32, 16, 1024, kLayoutSw128);
-                    mma_i8(tmem, ad, bd, id, (i > 0 || kk > 0) ? 1u : 0u);
+                    mma_i8(acc, ad, bd, id, (i > w || kk > 0) ? 1u : 0u);
                 }
                 mma_commit(&empty[s]);
             }
@@ -231,10 +247,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     cluster_sync_all();
     const int W = a.MP / a.S;
     uint32_t* recv = reinterpret_cast<uint32_t*>(smem);
-    if (warp >= 2) {
+    const bool epi = warp >= 2 && (!EX || warp < 2 + kEpiW);
+    if (epi) {
         const int q = warp & 3;  // the TMEM lane quarter this warp may access
         if (nkb > 0 && ok) {
-            send_partials(tmem, q, lane, a.MP, W, rank, recv);
+            send_partials(tmem, q, lane, a.MP, W, rank, recv, EX ? min(a.issuers, nkb) : 1, a.acc_cols);
         } else {
             // no contraction block (or a failed wait): zeros
             const int row = q * 32 + lane;
@@ -246,7 +263,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
     }
     cluster_sync_all();
-    if (warp >= 2) {
+    if (epi) {
         const int row = (warp & 3) * 32 + lane;
         const int n = n0 + row;
         const bool nok = n < a.N;
@@ -353,8 +370,9 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    pdl_trigger();
+    if constexpr (!EX) pdl_trigger();
     pdl_wait();
+    if constexpr (EX) pdl_trigger();  // after the wait: see launch_rank_x_q
 
     bool ok = true;
     if (warp == 0) {
@@ -488,7 +506,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     if (warp >= kEpi0) {
         const int q = warp & 3;  // the TMEM lane quarter this warp may access
         if (nnb > 0 && ok) {
-            send_partials(tmem, q, lane, a.MP, W, rank, recv);
+            send_partials(tmem, q, lane, a.MP, W, rank, recv, 1, 0);
         } else {
             const int row = q * 32 + lane;
             for (int c = 0; c < a.MP; ++c) {
@@ -622,6 +640,8 @@ cudaError_t plan(const void* kern, int threads, int tiles, uint32_t stage, bool 
     }
     const int fit = a.ring / static_cast<int>(stage);
     a.stages = fit > kMaxStages ? kMaxStages : fit;
+    a.issuers = 1;
+    a.tmem_cols = pow2_cols(a.MP);
     return cudaSuccess;
 }
 
@@ -653,7 +673,6 @@ cudaError_t launch_gemm_i8_fwd_small(Act act, const int8_t* Xq, const int8_t* Wq
     const int tiles = (N + kCh - 1) / kCh;
     a.S = pick_split(tiles, a.kblocks);
     const uint32_t stage = kCh * 128 + static_cast<uint32_t>(a.MP) * 128 + (w4 ? kCh * 64 : 0);
-    a.tmem_cols = pow2_cols(a.MP);
     CUtensorMap tw, tx;
     const bool wok = w4 ? make_tmap_2d(&tw, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, N, K / 2, K / 2, kCh, 64,
                                        CU_TENSOR_MAP_SWIZZLE_NONE)
@@ -666,7 +685,18 @@ cudaError_t launch_gemm_i8_fwd_small(Act act, const int8_t* Xq, const int8_t* Wq
         // (integer sums: the split does not change them)
         cudaError_t e = plan(reinterpret_cast<const void*>(kern), kFwdThreads, tiles, stage, true, true, a);
         if (e != cudaSuccess) return e;
-        return launch_k(kern, dim3(tiles, a.S), dim3(kFwdThreads), a.ring + kTail, s, a.S, tw, tx, a, ep, status);
+        // a tcgen05.mma of so few tokens holds its issuing thread longer than it
+        // runs: two issuers (the one-token forward of 2048 x 16384 18.5 us
+        // against 20.5 cold, three and four no better; the dX kernel, whose
+        // de-quantization sets the pace, gained nothing)
+        a.acc_cols = (a.MP + 31) / 32 * 32;
+        if (ep.ex && 2 * a.acc_cols <= 256 && a.stages >= 2) {
+            a.issuers = kMaxIssuers;
+            a.stages -= a.stages % kMaxIssuers;
+            a.tmem_cols = pow2_cols(kMaxIssuers * a.acc_cols);
+        }
+        return launch_k(kern, dim3(tiles, a.S), dim3(kFwdThreads + 32 * (a.issuers - 1)), a.ring + kTail, s, a.S, tw,
+                        tx, a, ep, status);
     };
     // by rank, then by codes and epilogue form
 #define QL_FWD_SMALL(T, R)                                                                          \
@@ -694,7 +724,6 @@ cudaError_t launch_gemm_dx_small(const void* dY, const int8_t* Wq, const float* 
     const int tiles = (K + kCh - 1) / kCh;
     a.S = pick_split(tiles, a.kblocks);
     const uint32_t stage = kDqTileBytes + kCodeBytes + static_cast<uint32_t>(a.MP) * 128;
-    a.tmem_cols = pow2_cols(a.MP);
     CUtensorMap ty, tw;
     if (!make_tmap_2d(&ty, dY, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, M, N, static_cast<uint64_t>(N) * 2, a.MP,
                       64, CU_TENSOR_MAP_SWIZZLE_128B) ||

@@ -62,7 +62,7 @@ FORWARD = [
     (65, 784, 128, 4), (100, 4096, 128, 8), (130, 2048, 200, 16), (333, 784, 1001, 8), (300, 272, 96, 20),
     (128, 144, 40, 64), (250, 4112, 70, 4), (513, 1040, 3000, 4), (2048, 272, 2600, 4), (2050, 512, 2568, 16), (1600, 256, 3333, 8),
     (2048, 2064, 2560, 4), (2048, 2064, 2576, 8), (9000, 2048, 264, 4), (9000, 1920, 40, 8), (5000, 4096, 24, 4),
-    (5000, 3600, 24, 8),
+    (5000, 3600, 24, 8), (16, 8192, 2000, 4), (1, 4096, 2048, 8), (64, 4096, 2048, 16), (33, 1024, 2300, 4),
 ]
 
 
@@ -127,6 +127,7 @@ BACKWARD = [
     (1, 16, 8, 1), (1, 2048, 512, 4), (16, 1024, 2048, 4), (17, 784, 136, 3), (64, 528, 264, 16), (65, 784, 128, 4),
     (127, 48, 64, 8), (129, 272, 200, 16), (333, 784, 1000, 8), (300, 272, 96, 20), (140, 144, 40, 33),
     (256, 144, 72, 64), (77, 160, 10, 4), (202, 80, 12608, 4), (256, 48, 2048, 16), (70, 2048, 1032, 8), (1024, 2576, 128, 4), (1030, 2560, 192, 16), (2500, 528, 320, 8), (1100, 1280, 136, 4), (2100, 1040, 2056, 2),
+    (16, 2176, 4096, 4), (40, 2048, 1000, 40),
 ]
 
 
@@ -167,7 +168,8 @@ def _pack_int4(codes):
 
 @pytest.mark.parametrize("M,K,N,r,dt", [(5, 256, 160, 4, BF16), (200, 288, 161, 8, BF16), (150, 96, 72, 4, F32),
                                         (2100, 256, 2568, 4, BF16), (2100, 256, 2565, 16, BF16),
-                                        (1100, 1280, 136, 4, BF16)])
+                                        (1100, 1280, 136, 4, BF16), (64, 2048, 2048, 4, BF16),
+                                        (16, 4096, 1984, 4, BF16)])
 def test_int4_kernels_match_their_int8_codes(M, K, N, r, dt):
     """Packed int4 codes give what the same codes give as int8: to the last bit
     on the same kernel form, to half a step where the forms differ."""
@@ -448,6 +450,46 @@ def test_streams_and_two_calls_at_once(size):
     for Y, keep, gr in out:
         assert torch.equal(Y, Y0) and torch.equal(keep.zq, keep0.zq) and torch.equal(keep.zs, keep0.zs)
         assert all(torch.equal(a, b) for a, b in zip(gr, g0))
+
+
+@pytest.mark.parametrize("M,K,N,dt", [(16, 1024, 1024, BF16), (64, 784, 784, F32), (300, 784, 784, BF16),
+                                      (1100, 1280, 1280, BF16)])
+def test_calls_back_to_back_see_each_others_results(M, K, N, dt):
+    """A run of backward passes, each fed by the one before and all on one
+    workspace, with nothing between them: the X pass may run beside the dX GEMM
+    before it, and the next call's first kernel reads that dX.  The same bits
+    as with the device idle before each call, whatever lay in the caches."""
+    r, n = 4, 12
+    g = _gen(77)
+    layers = [make_layer(K, N, r, dt, g) for _ in range(3)]
+    for L in layers:
+        L.sw.mul_(0.6)  # the gradient keeps its size from call to call
+    keeps, zs = [], []
+    for _ in range(3):
+        X = torch.randn(M, K, generator=g, device="cuda").to(dt)
+        q, sx = ref.row_codes(X)
+        keeps.append(qlora.Checkpoint(q, sx, X.float() @ layers[len(keeps)].A))
+        zs.append(ref.block_codes(torch.randn(M, K, generator=g, device="cuda") * 1.5))
+    first = (torch.randn(M, N, generator=g, device="cuda") * 0.3).to(dt)
+    ws = qlora.ckpt_workspace(layers[0].desc(), M)
+
+    def chain(idle):
+        dY, out = first, []
+        for i in range(n):
+            if idle:
+                torch.cuda.synchronize()
+                ws.fill_(0xC3)
+                torch.cuda.synchronize()
+            res = qlora.backward_ckpt(layers[i % 3], keeps[i % 3], dY, ws, act="silu", z=zs[i % 3], add=dY)
+            out.append(res)
+            dY = res[0]
+        return out
+
+    want = chain(True)
+    assert all(torch.isfinite(t).all() for t in want[-1])
+    for _ in range(10):
+        for a, b in zip(chain(False), want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 def test_offsets_beyond_32_bits():
