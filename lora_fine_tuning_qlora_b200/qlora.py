@@ -711,13 +711,15 @@ def _expect(t, name: str, shape, dtype, device):
     """Checks one tensor argument; returns its address (None for None)."""
     if t is None:
         return None
-    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+    if t.shape == shape and t.dtype is dtype and t.get_device() == device.index and t.is_contiguous():
         return t.data_ptr()
     if t.shape != shape or t.dtype != dtype:
         raise ValueError("%s must be %s of shape %s" % (name, dtype, tuple(shape)))
     if t.device != device:
         raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
-    raise ValueError("%s must be contiguous" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
 
 def _on_device(t: torch.Tensor, what: str, stream):
@@ -733,9 +735,12 @@ def _on_device(t: torch.Tensor, what: str, stream):
     return dev, torch._C._cuda_getCurrentRawStream(dev.index)  # current_stream() without its object
 
 
+_no_stream = contextlib.nullcontext()
+
+
 def _allocating_on(stream):
     """Outputs are allocated on the stream that writes them."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return _no_stream if stream is None else torch.cuda.stream(stream)
 
 
 def ckpt_buffers(M: int, N: int, device=None):
@@ -779,14 +784,16 @@ def forward_act(layer: Layer, X: torch.Tensor, act: str = "none", residual: Opti
     wq, sw, bias, a, b = _check_layer_tensors(layer, dev)
     with _allocating_on(stream):
         if Y is None:
-            Y = torch.empty((M, N), dtype=layer.act, device=dev)
+            Y = X.new_empty((M, N))
+            y = Y.data_ptr()
+        else:
+            y = _expect(Y, "Y", (M, N), layer.act, dev)
         if keep is None:
             keep = Checkpoint.allocate(M, K, r, dev)
             if save_z:
                 keep.zq, keep.zs = ckpt_buffers(M, N, dev)
     if save_z and keep.zq is None:
         raise ValueError("save_z needs zq and zs in keep")
-    y = _expect(Y, "Y", (M, N), layer.act, dev)
     xq, sx, xa = keep._addresses(M, K, r, dev)
     ep = FwdEpilogue(fn, _expect(residual, "residual", (M, N), layer.act, dev), None, None)
     if save_z:
@@ -829,24 +836,29 @@ def backward_ckpt(layer: Layer, keep: Checkpoint, dY: torch.Tensor, ws: torch.Te
     w = _expect(ws, "ws", ws.shape, torch.uint8, dev)
     with _allocating_on(stream):
         if not want_dx:
-            dX = None
+            dX = dx = None
         elif dX is None:
-            dX = torch.empty((M, K), dtype=layer.act, device=dev)
+            dX = dY.new_empty((M, K))
+            dx = dX.data_ptr()
+        else:
+            dx = _expect(dX, "dX", (M, K), layer.act, dev)
         if grads is not None:
             dA, dB, dbias = grads
-        else:
-            dA = torch.empty((K, r), dtype=f32, device=dev)
-            dB = torch.empty((r, N), dtype=f32, device=dev)
-            dbias = torch.empty((N,), dtype=f32, device=dev) if want_dbias else None
-        da, db = _expect(dA, "dA", (K, r), f32, dev), _expect(dB, "dB", (r, N), f32, dev)
-        dbi = _expect(dbias, "dbias", (N,), f32, dev)
+            da, db = _expect(dA, "dA", (K, r), f32, dev), _expect(dB, "dB", (r, N), f32, dev)
+            dbi = _expect(dbias, "dbias", (N,), f32, dev)
+        else:  # shaped as the parameters, which have been checked
+            dA, dB, dbias = torch.empty_like(layer.A), torch.empty_like(layer.B), None
+            da, db, dbi = dA.data_ptr(), dB.data_ptr(), None
+            if want_dbias:
+                dbias = torch.empty_like(layer.sw)
+                dbi = dbias.data_ptr()
         if M == 0:
             for g in (dA, dB, dbias):
                 if g is not None:
                     g.zero_()
             return dX, dA, dB, dbias
-    _check(_lib.qlora_backward_ckpt(layer.desc(), M, xq, sx, dy, wq, sw, a, b, xa, ep,
-                                    _expect(dX, "dX", (M, K), layer.act, dev), da, db, dbi, w, ws.numel(), s))
+    _check(_lib.qlora_backward_ckpt(layer.desc(), M, xq, sx, dy, wq, sw, a, b, xa, ep, dx, da, db, dbi, w, ws.numel(),
+                                    s))
     return dX, dA, dB, dbias
 
 
@@ -888,14 +900,17 @@ def ckpt_save(T: torch.Tensor, out=None, stream=None):
     if T.dim() != 2:
         raise ValueError("T must have two axes")
     M, N = T.shape
+    code, t = act_code(T.dtype), _expect(T, "T", (M, N), T.dtype, dev)
     if out is None:
         with _allocating_on(stream):
-            out = ckpt_buffers(M, N, dev)
-    q, scales = out
-    args = (_expect(T, "T", (M, N), T.dtype, dev), M, N, act_code(T.dtype), _expect(q, "q", (M, N), torch.int8, dev),
-            _expect(scales, "scales", (-(-N // CKPT_BLOCK), M), torch.float32, dev), s)
+            q, scales = ckpt_buffers(M, N, dev)
+        pq, ps = q.data_ptr(), scales.data_ptr()
+    else:
+        q, scales = out
+        pq = _expect(q, "q", (M, N), torch.int8, dev)
+        ps = _expect(scales, "scales", (-(-N // CKPT_BLOCK), M), torch.float32, dev)
     if M > 0:
-        _check(_lib.qlora_ckpt_save(*args))
+        _check(_lib.qlora_ckpt_save(t, M, N, code, pq, ps, s))
     return q, scales
 
 
@@ -908,12 +923,15 @@ def ckpt_load(q: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.
         raise ValueError("q must have two axes")
     M, N = q.shape
     block = 0 if scales.dim() == 1 else CKPT_BLOCK
+    shape = (M,) if block == 0 else (-(-N // CKPT_BLOCK), M)
+    pq, ps = _expect(q, "q", (M, N), torch.int8, dev), _expect(scales, "scales", shape, torch.float32, dev)
+    code = act_code(dtype if out is None else out.dtype)
     if out is None:
         with _allocating_on(stream):
             out = torch.empty((M, N), dtype=dtype, device=dev)
-    shape = (M,) if block == 0 else (-(-N // CKPT_BLOCK), M)
-    args = (_expect(q, "q", (M, N), torch.int8, dev), _expect(scales, "scales", shape, torch.float32, dev), M, N, block,
-            act_code(out.dtype), _expect(out, "out", (M, N), out.dtype, dev), s)
+        t = out.data_ptr()
+    else:
+        t = _expect(out, "out", (M, N), out.dtype, dev)
     if M > 0:
-        _check(_lib.qlora_ckpt_load(*args))
+        _check(_lib.qlora_ckpt_load(pq, ps, M, N, block, code, t, s))
     return out
