@@ -6,14 +6,15 @@
 //   split  few rows: a row is spread over a cluster of S CTAs, each 256
 //          threads with one 16-byte chunk (or more) of it; the row's maximum
 //          and the partial sums meet in distributed shared memory.  Bound by
-//          latency (two block reductions and two cluster barriers); at 16 x
-//          16384 the one CTA that walked all 16 rows took about 85 us.
+//          latency (two block reductions and two cluster barriers): 1 x 2048 3.8
+//          us, 16 x 16384 5.2 us (one CTA that walked all 16 rows: 85 us).
 //   rows   many bf16 rows of at most 4096: each warp holds R whole rows in
 //          registers, so that the maximum and the sums need no other warp
 //          and no barrier, and the factor A is read from shared memory once
 //          per R rows.  HBM: 2 + 1 bytes per element; what bounds it is the
 //          instruction count per element (unpack, maximum, multiply, convert,
-//          pack, r / 2 paired FMAs, 2 / R shared loads for rank 4).
+//          pack, r / 2 paired FMAs, 2 / R shared loads for rank 4): 16384 x
+//          4096 rank 4 in 47 us, 4.3 TB/s.
 #include "internal.h"
 #include "ptx.cuh"
 

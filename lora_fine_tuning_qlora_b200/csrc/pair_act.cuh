@@ -21,8 +21,10 @@
 // many warps (W, two or four per scheduler), takes its rank-r sums in paired
 // fp32 instructions, and fetches the next tile's row and column factors while
 // the current one is computed.  Forward, 16384 x 4096 x 4096 bf16 rank 4,
-// GELU(tanh) + residual + checkpoint: four epilogue warps 289 us; see the
-// launch rule below for W.
+// GELU(tanh) + residual + checkpoint: 289 us with four epilogue warps, 237 with
+// eight (the forward's launch rule has W).  With SILU + residual 204 us, 2.7
+// PTOP/s; dX of that size 400 us, 1.37 PFLOP/s, the rate at which plain bf16
+// products run under the power cap.
 //
 // Warps per CTA: 0 TMA producer; 1 TMEM owner and, in CTA 0, MMA issuer; then
 // W epilogue warps, W / 4 per TMEM lane quarter, each with its own columns.

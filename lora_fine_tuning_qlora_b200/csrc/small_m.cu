@@ -1,4 +1,5 @@
-// small_m.cu -- the two GEMMs of the layer for few tokens (M <= 64), where
+// small_m.cu -- the two GEMMs of the layer for few tokens (M <= 64; with an
+// activation epilogue up to 256 where the large tiles would be few), where
 // the int8 kernel Wq [N,K] dominates the traffic and every SM must stream a
 // share of it ("How to fine-tune the 4-bit model?" thread: with few tokens
 // the layer is bound by reading the weights, not by arithmetic).
