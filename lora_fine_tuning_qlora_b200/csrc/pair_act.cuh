@@ -28,7 +28,10 @@
 //
 // Warps per CTA: 0 TMA producer; 1 TMEM owner and, in CTA 0, MMA issuer; then
 // W epilogue warps, W / 4 per TMEM lane quarter, each with its own columns.
-// Barriers as in the other pair kernels; every wait is bounded.
+// Barriers as in the other pair kernels; every wait is bounded.  The pieces'
+// barriers belong to one warp each, so one epilogue warp can give up alone: it
+// then skips its tiles but still counts at the named barriers of all of them,
+// which have no limit of their own.
 #pragma once
 
 #include "dx_common.cuh"
@@ -305,6 +308,7 @@ __global__ void __launch_bounds__(PairActCfg<RP, FWD, W>::kThreads, 1)
         };
         fetch_factors(pair);
         fetch_tile(pair);
+        bool ok = true;  // false once a wait of this warp gave up
         int i = 0;
         for (int t = pair; t < tiles; t += npairs, ++i) {
             const int ab = i & 1;
@@ -332,8 +336,8 @@ __global__ void __launch_bounds__(PairActCfg<RP, FWD, W>::kThreads, 1)
             for (int j = 0; j < RP; ++j) rf[j] = pk2(frow[j] * a.c, frow[j] * a.c);
             const unsigned long long sx2 = pk2(fsx, fsx);
             fetch_factors(t + npairs);
-            bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
-            if (!ok) break;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
+            if (!ok) continue;  // the other warps may still meet at the next tile's named barriers
             tc_fence_after();
             const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * kTN;
             bool given_back = false;
@@ -365,7 +369,10 @@ __global__ void __launch_bounds__(PairActCfg<RP, FWD, W>::kThreads, 1)
                 tmem_ld16(tbase + col + kEpiCols, v1);
                 if (loads) {
                     ok = __all_sync(0xffffffffu, mbar_wait(&pbar[piece & 1], (piece >> 1) & 1, status));
-                    if (!ok) break;
+                    if (!ok) {
+                        tmem_ld_wait();
+                        break;
+                    }
                 }
                 tmem_ld_wait();
                 if (last) give_back();
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(PairActCfg<RP, FWD, W>::kThreads, 1)
                     bulk_commit();
                 }
             }
-            if (!ok) break;
+            if (!ok) continue;
             if (!given_back) give_back();
         }
         // after a give-up: this warp's loads still in flight
