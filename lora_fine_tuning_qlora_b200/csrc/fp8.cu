@@ -658,6 +658,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
         const bool vec = ((static_cast<size_t>(N) * sizeof(OutT)) % 16) == 0;
         const uint32_t tempty0 = dsmem_addr(tempty, 0);
         const float sab = __fmul_rn(__ldg(sa), __ldg(sb));
+        bool ok = true;  // false once a wait of this warp gave up: it still counts at the named barriers
         int i = 0;
         for (int u = 0; u < nunits; ++u, ++i) {
             int t, kb0, kb1, half;
@@ -673,8 +674,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 sBias[col] = (bias && n < N) ? __ldg(bias + n) : 0.f;
             }
             named_bar_sync(1, 32 * kGEpi);
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
-            if (!ok) break;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
+            if (!ok) continue;
             tc_fence_after();
             const int row0 = m0 + q * 32;
             const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * P::kAccCols;

@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(k2_threads<W4>(), 1)
         uint8_t* stg = smem + C::kStgOff + ew * 32 * stage_pitch<OutT>();
         const bool vec = ((static_cast<size_t>(N) * sizeof(OutT)) % 16) == 0;
         OutT* Y = static_cast<OutT*>(ep.Y);
+        bool ok = true;  // false once a wait of this warp gave up: it still counts at the named barriers
         int i = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
             const int ab = i & 1;
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(k2_threads<W4>(), 1)
                     xa[j] = (row_ok && j < ep.r) ? ep.xA[static_cast<size_t>(row) * ep.r + j] * ep.c : 0.f;
             }
 
-            bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
             tc_fence_after();
             const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * C::kAccCols;
             // split-K: this CTA's rows of the tile and where this lane's row lives
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(k2_threads<W4>(), 1)
                 tc_fence_after();
                 if (own_lo >= q * 32 + 32 || own_lo + R <= q * 32) break;  // no rows of mine here
             }
-            if (!ok) break;
+            if (!ok) continue;
             const int row_min = SPLIT ? m0 + own_lo : 0;
             const int row_lim = SPLIT ? min(M, m0 + own_lo + R) : M;
             const bool own_row = !SPLIT || (trow >= own_lo && trow < own_lo + R);

@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(q_threads<W4, EX>(), 1)
         __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(ep.Y);
         const bool vec = ((static_cast<size_t>(N) * 2) % 16) == 0;
         const uint32_t tempty0 = dsmem_addr(tempty, 0);
+        bool ok = true;  // false once a wait of this warp gave up: it still counts at the named barriers
         int i = 0;
         for (int t = pair; t < tiles; t += npairs, ++i) {
             const int ab = i & 1;
@@ -325,8 +326,8 @@ __global__ void __launch_bounds__(q_threads<W4, EX>(), 1)
                 const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(ep.res);
                 RowPiece<__nv_bfloat16, 32> rp;
                 if (res) rp.load(res, row, row_ok, n0 + c0, N, vec);
-                const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
-                if (!ok) break;
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
+                if (!ok) continue;
                 tc_fence_after();
                 const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * C::kAccCols;
 #pragma unroll 1
@@ -358,8 +359,8 @@ __global__ void __launch_bounds__(q_threads<W4, EX>(), 1)
                     }
                 }
             } else {
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
-            if (!ok) break;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
+            if (!ok) continue;
             tc_fence_after();
             const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * C::kAccCols;
 #pragma unroll 1

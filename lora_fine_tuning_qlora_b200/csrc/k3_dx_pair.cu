@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         uint8_t* stg = smem + C::kStgOff + ew * 32 * stage_pitch<__nv_bfloat16>();
         __nv_bfloat16* dX = static_cast<__nv_bfloat16*>(ep.dX);
         const uint32_t tempty0 = dsmem_addr(tempty, 0);
+        bool ok = true;  // false once a wait of this warp gave up: it still counts at the named barriers
         int i = 0;
         for (int t = pair; t < tiles; t += npairs, ++i) {
             const int ab = i & 1;
@@ -373,8 +374,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int j = 0; j < RP; ++j) gr[j] = (row_ok && j < ep.r) ? g_row(ep, M, row, j) * ep.c : 0.f;
             DxPiece<__nv_bfloat16> px;
             if constexpr (EX) px.load(ep, M, K, row, row_ok, k0, true);
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
-            if (!ok) break;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], use & 1, status));
+            if (!ok) continue;
             tc_fence_after();
             const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * C::kAccCols;
 #pragma unroll 1

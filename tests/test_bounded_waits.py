@@ -10,7 +10,14 @@ import re
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "lora_fine_tuning_qlora_b200", "csrc")
-SOURCES = ["pair_act.cuh"]
+
+
+def _with_barriers():
+    names = sorted(n for n in os.listdir(CSRC) if n.endswith((".cu", ".cuh")))
+    return [n for n in names if n != "tile_epilogue.cuh" and "named_bar_sync(" in open(os.path.join(CSRC, n)).read()]
+
+
+SOURCES = _with_barriers()
 
 
 def plain_source(text):
@@ -99,7 +106,7 @@ def test_the_model():
 def test_a_give_up_leaves_no_warp_at_a_named_barrier(name):
     with open(os.path.join(CSRC, name)) as f:
         bodies = list(barrier_loops(plain_source(f.read())))
-    assert bodies
+    assert bodies or name == "k4_rank_q.cu"  # (its barriers stand in no loop)
     for body in bodies:
         steps = events(body)
         assert steps and not stuck(steps), (name, steps)
