@@ -200,7 +200,9 @@ int qlora_backward_noalloc(const qlora_layer_desc* d, int M, const void* X, cons
 
 /* a1: per-row abs-max quantization of X into Xq [M,K] int8 and sx [M] fp32
  * (bit-exact with the reading above), and xA = X . A [M,r] fp32 from the
- * same read of X ("LoRA equation": the adapter sees the layer input). */
+ * same read of X ("LoRA equation": the adapter sees the layer input).  A row
+ * that holds a NaN gets sx NaN, one with an infinity and no NaN sx infinite,
+ * either with codes 0: all of it reads back as NaN, as its output row is. */
 int qlora_quantize_input(const qlora_layer_desc* d, int M, const void* X, const float* A,
                          int8_t* Xq, float* sx, float* xA, void* stream);
 

@@ -89,14 +89,14 @@ __global__ void __launch_bounds__(kSplitThreads) k1_split_kernel(const T* __rest
     if (c0 + t < c1) load8(xr + static_cast<size_t>(c0 + t) * 8, v0);
     float amax = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v0[e]));
+    for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(v0[e]));
     for (int c = c0 + t + kSplitThreads; c < c1; c += kSplitThreads) {
         float v[8];
         load8(xr + static_cast<size_t>(c) * 8, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+        for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(v[e]));
     }
-    const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));  // amax >= 0
+    const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));  // amax >= 0 or NaN, whose bits are above all
     if (lane == 0) wmax[warp] = wm;
     // x . A needs no maximum: its loads go out before the barriers
     float acc[RP];
@@ -220,9 +220,9 @@ __global__ void __launch_bounds__(kRowsThreads) k1_rows_kernel(const __nv_bfloat
                 const uint32_t w[4] = {x[q][i].x, x[q][i].y, x[q][i].z, x[q][i].w};
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
-                    m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[h])));
+                    m2 = __hmax2_nan(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[h])));
             }
-            const float top = fmaxf(__low2float(m2), __high2float(m2));
+            const float top = max_nan(__low2float(m2), __high2float(m2));
             const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
             inv[q] = amax > 0.f ? __fdiv_rn(127.0f, amax) : 0.f;
             if (lane == 0 && g * R + q < M) sx[g * R + q] = __fdiv_rn(amax, 127.0f);

@@ -5,7 +5,9 @@
 // The quantizer ("Introduce QLoRA-like technique": frozen int8 Dense with
 // dynamically quantized inputs) is symmetric abs-max in IEEE fp32 with one
 // rounding per operation: inv = 127 / amax, q = clamp(rne(v * inv), -127,
-// 127), s = amax / 127.  The LoRA term uses the unquantized input
+// 127), s = amax / 127.  A row that holds a NaN gets scale NaN and codes 0, one
+// with an infinity and no NaN scale inf and codes 0: either reads back as NaN.
+// The LoRA term uses the unquantized input
 // ("Parameter-efficient fine-tuning of GPT-2 with LoRA", "LoRA equation").
 //
 // K1 is HBM-bound: it reads M*K*e bytes of X once (128-bit loads held in
@@ -146,7 +148,7 @@ __device__ __forceinline__ float row_reduce(float v, float* red, int row_in_bloc
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         float w = __shfl_xor_sync(0xffffffffu, v, o);
-        v = IS_MAX ? fmaxf(v, w) : v + w;
+        v = IS_MAX ? max_nan(v, w) : v + w;
     }
     if constexpr (TPR > 32) {
         constexpr int W = TPR / 32;
@@ -156,7 +158,7 @@ __device__ __forceinline__ float row_reduce(float v, float* red, int row_in_bloc
 #pragma unroll
         for (int i = 1; i < W; ++i) {
             float w = red[row_in_block * W + i];
-            s = IS_MAX ? fmaxf(s, w) : s + w;
+            s = IS_MAX ? max_nan(s, w) : s + w;
         }
         __syncthreads();
         v = s;
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) k1_quantize_rows_kernel(
 #pragma unroll
         for (int i = 0; i < kMaxCPT; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[i][e]));
+            for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(v[i][e]));
         amax = row_reduce<TPR, true>(amax, red, row_in_block, t);
         const float inv = amax > 0.f ? __fdiv_rn(127.0f, amax) : 0.f;
         if (live) {
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) k1_quantize_rows_long_kernel(
         float v[8];
         Chunk8<T>::load(xr + ch * kChunk, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+        for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(v[e]));
     }
     amax = row_reduce<kThreads, true>(amax, red, 0, t);
     const float inv = amax > 0.f ? __fdiv_rn(127.0f, amax) : 0.f;
@@ -340,11 +342,11 @@ __global__ void __launch_bounds__(kThreads) k1_quantize_rows_sliced_kernel(
                 for (int u = 0; u < kU; ++u)
                     if (ch + 32 * u < nchunks)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[u][e]));
+                        for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(v[u][e]));
             }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         inv[q] = amax > 0.f ? __fdiv_rn(127.0f, amax) : 0.f;
         if (m < M && lane == 0) sx[m] = __fdiv_rn(amax, 127.0f);
     }
@@ -597,17 +599,17 @@ __global__ void __launch_bounds__(staged::cons<TPR, RP>() + 32, 1)
                         const uint32_t wv[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                         for (int h = 0; h < 4; ++h)
-                            m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&wv[h])));
+                            m2 = __hmax2_nan(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&wv[h])));
                     }
                 }
             }
-            amax[q] = fmaxf(__low2float(m2), __high2float(m2));
+            amax[q] = max_nan(__low2float(m2), __high2float(m2));
         }
         {
             float v[kRPG];
 #pragma unroll
             for (int q = 0; q < kRPG; ++q) v[q] = amax[q];
-            const float x = xreduce<kRPG, true>(v);
+            const float x = xreduce<kRPG, true, true>(v);
             if constexpr (W == 1) {
 #pragma unroll
                 for (int q = 0; q < kRPG; ++q) amax[q] = __shfl_sync(0xffffffffu, x, xreduce_lane<kRPG>(q));
@@ -625,9 +627,9 @@ __global__ void __launch_bounds__(staged::cons<TPR, RP>() + 32, 1)
                 float mx = 0.f;
 #pragma unroll
                 for (int ww = lane & (kLPR - 1); ww < W; ww += kLPR)
-                    mx = fmaxf(mx, redA[(g * kRPG + qr) * W + ww]);
+                    mx = max_nan(mx, redA[(g * kRPG + qr) * W + ww]);
 #pragma unroll
-                for (int off = 1; off < kLPR; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                for (int off = 1; off < kLPR; off <<= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
 #pragma unroll
                 // one division per row, in the row's lanes
                 const float iv = mx > 0.f ? __fdiv_rn(127.0f, mx) : 0.f;

@@ -528,11 +528,21 @@ __device__ __forceinline__ void fma2(unsigned long long& d, unsigned long long a
 // ---------------------------------------------------------------------------
 // warp reductions
 // ---------------------------------------------------------------------------
-// Sum (or max) of the V values v[] over the warp's 32 lanes, transposed:
+// max(a, b), NaN if either is NaN (fmaxf would drop it): an abs-max that meets
+// a NaN has to say so.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Sum (or max; with NANS one that keeps a NaN) of the V values v[] over the
+// warp's 32 lanes, transposed:
 // returns one total per lane, lane l holding value xreduce_index<V>(l).
 // Every halving step sends half of the live values and keeps the other half.
-template <int V, bool MAX>
+template <int V, bool MAX, bool NANS = false>
 __device__ __forceinline__ float xreduce(float (&v)[V]) {
+    const auto top = [](float a, float b) { return NANS ? max_nan(a, b) : fmaxf(a, b); };
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int n = V, off = 16; n > 1; n >>= 1, off >>= 1) {
@@ -542,14 +552,14 @@ __device__ __forceinline__ float xreduce(float (&v)[V]) {
             const float send = up ? v[i] : v[i + n / 2];
             const float keep = up ? v[i + n / 2] : v[i];
             const float recv = __shfl_xor_sync(0xffffffffu, send, off);
-            v[i] = MAX ? fmaxf(keep, recv) : keep + recv;
+            v[i] = MAX ? top(keep, recv) : keep + recv;
         }
     }
     float x = v[0];
 #pragma unroll
     for (int off = 32 / V / 2; off >= 1; off >>= 1) {
         const float y = __shfl_xor_sync(0xffffffffu, x, off);
-        x = MAX ? fmaxf(x, y) : x + y;
+        x = MAX ? top(x, y) : x + y;
     }
     return x;
 }
