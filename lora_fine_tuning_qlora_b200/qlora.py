@@ -655,13 +655,17 @@ class Checkpoint:
 
     ``Checkpoint(Xq, sx, xA, zq, zs)`` holds given tensors;
     ``Checkpoint.allocate(M, K, r, device)`` makes one allocation for Xq, sx
-    and xA, whose tensors are views made when they are asked for."""
+    and xA, whose tensors are views made when they are asked for.  ``z`` is None
+    after a forward that kept no Z here (``forward_act(keep=..., save_z=False)``,
+    or a refused one): what zq and zs then hold belongs to an earlier input.
+    Given zq and zs count as this input's."""
 
     def __init__(self, Xq: Optional[torch.Tensor] = None, sx: Optional[torch.Tensor] = None,
                  xA: Optional[torch.Tensor] = None, zq: Optional[torch.Tensor] = None,
                  zs: Optional[torch.Tensor] = None):
         self._Xq, self._sx, self._xA = Xq, sx, xA
-        self.zq, self.zs = zq, zs
+        self._zq, self._zs = zq, zs
+        self._z_kept = True  # whether zq and zs belong to Xq, sx and xA
         self._block = None  # (fp32 buffer, M, K, r): xA, then sx, then Xq from a 16-byte boundary
 
     @classmethod
@@ -702,9 +706,25 @@ class Checkpoint:
                 _expect(self.xA, "xA", (M, r), torch.float32, device))
 
     @property
+    def zq(self) -> Optional[torch.Tensor]:
+        return self._zq
+
+    @zq.setter
+    def zq(self, t: Optional[torch.Tensor]):
+        self._zq, self._z_kept = t, True
+
+    @property
+    def zs(self) -> Optional[torch.Tensor]:
+        return self._zs
+
+    @zs.setter
+    def zs(self, t: Optional[torch.Tensor]):
+        self._zs, self._z_kept = t, True
+
+    @property
     def z(self):
         """(zq, zs), as the backward of the layer above takes it."""
-        return None if self.zq is None else (self.zq, self.zs)
+        return (self._zq, self._zs) if self._zq is not None and self._z_kept else None
 
 
 def _expect(t, name: str, shape, dtype, device):
@@ -775,7 +795,8 @@ def forward_act(layer: Layer, X: torch.Tensor, act: str = "none", residual: Opti
     """Y = act(Z) + residual with Z the layer's output; returns (Y, Checkpoint).
 
     The checkpoint holds the input's codes (and, with ``save_z``, Z in 8
-    bits); ``keep`` gives its buffers, else they are allocated.  ``residual``
+    bits); ``keep`` gives its buffers, else they are allocated (without
+    ``save_z`` its ``z`` is None afterwards).  ``residual``
     may be ``Y`` itself.  Gradients: ``backward_ckpt``."""
     fn = act_fn(act)
     dev, s = _on_device(X, "X", stream)
@@ -799,8 +820,10 @@ def forward_act(layer: Layer, X: torch.Tensor, act: str = "none", residual: Opti
     if save_z:
         ep.zq = _expect(keep.zq, "zq", (M, N), torch.int8, dev)
         ep.zs = _expect(keep.zs, "zs", (-(-N // CKPT_BLOCK), M), torch.float32, dev)
+    keep._z_kept = False
     if M > 0:
         _check(_lib.qlora_forward_act(layer.desc(), M, x, wq, sw, bias, a, b, ep, y, xq, sx, xa, s))
+    keep._z_kept = save_z
     return Y, keep
 
 
