@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(k2_threads<W4>(), 1)
                     step16(col, v, z);
                     step16(col + kEpiCols, v, z + kEpiCols);
                     if (ep.zq && mine) ckpt_store(z, ep.zq, ep.zs, row, M, n0 + col, N);
-                    act_apply(ep.act, z);
+                    act_apply<OutT>(ep.act, z);
                     if (res) {
                         rp.add_to(z);
                         if (col + 32 < c0 + kCols) rp.load(res, row, mine, n0 + col + 32, N, vec);

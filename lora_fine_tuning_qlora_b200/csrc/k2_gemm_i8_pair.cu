@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(q_threads<W4, EX>(), 1)
                     finish16(v0, col, z);
                     finish16(v1, col + kEpiCols, z + kEpiCols);
                     if (ep.zq && row_ok) ckpt_store(z, ep.zq, ep.zs, row, M, n0 + col, N);
-                    act_apply(ep.act, z);
+                    act_apply<__nv_bfloat16>(ep.act, z);
                     if (res) {
                         rp.add_to(z);
                         if (col + 32 < c0 + kCols) rp.load(res, row, row_ok, n0 + col + 32, N, vec);

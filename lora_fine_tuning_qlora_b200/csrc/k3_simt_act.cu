@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) k3_simt_act_kernel(const T* __restri
             float z[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[e] = static_cast<float>(static_cast<int8_t>(q >> (8 * e))) * s;
-            slope_apply(ep.act, z, acc[i]);
+            slope_apply<T>(ep.act, z, acc[i]);
         }
         const T* add = static_cast<const T*>(ep.add);
 #pragma unroll

@@ -415,13 +415,13 @@ __global__ void __launch_bounds__(PairActCfg<RP, FWD, W>::kThreads, 1)
                             ckpt_store(y, a.zq, a.zs_out, row, M, n0 + col, N);
                         }
                     }
-                    act_apply(a.act, y);
+                    act_apply<__nv_bfloat16>(a.act, y);
                 } else if (zin) {
                     uint8_t* zc = codes + (piece % C::kCodeBufs) * kCodePieceBytes;
                     float z[32];
                     ckpt_values16(*code_chunk(zc, lane, 0), zscale, *reinterpret_cast<float(*)[16]>(z));
                     ckpt_values16(*code_chunk(zc, lane, 1), zscale, *reinterpret_cast<float(*)[16]>(z + 16));
-                    slope_apply(a.act, z, y);
+                    slope_apply<__nv_bfloat16>(a.act, z, y);
                 }
                 if (a.add) piece_add(pc, lane, y);
                 piece_put(pc, lane, y);

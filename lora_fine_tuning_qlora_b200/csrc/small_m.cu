@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kFwdThreads + 32 * (EX ? kMaxIssuers - 1 : 0),
                     if (lane == 0 && nok) ep.zs[static_cast<size_t>(n / kCkptBlock) * a.M + m] = scale;
                 }
                 float z[1] = {y};
-                act_apply(ep.act, z);
+                act_apply<OutT>(ep.act, z);
                 if (nok) Y[static_cast<size_t>(m) * a.N + n] = ActIO<OutT>::from_f(res ? z[0] + rv : z[0]);
                 continue;
             }
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
                 const float av = anext;
                 fetch(cl + 1);
                 float yv[1] = {y};
-                slope_apply(ep.act, zv, yv);
+                slope_apply<__nv_bfloat16>(ep.act, zv, yv);
                 y = add ? yv[0] + av : yv[0];
             }
             if (gate && !(__bfloat162float(gate[static_cast<size_t>(m) * a.K + k]) > 0.f)) y = 0.f;
