@@ -17,7 +17,9 @@ namespace {
 constexpr int kDqThreads = 256;
 
 // 16 codes (int8) or 32 (packed int4) a thread and step; the same rounding as
-// in the kernels that de-quantize in shared memory.
+// in the kernels that de-quantize in shared memory: to bf16, since the products
+// take both operands in one 16-bit type and dY needs the range of bf16.  A second
+// bf16 term of the kernel would double the products, which bound these layers.
 template <bool W4>
 __global__ void __launch_bounds__(kDqThreads) dequantize_kernel(const uint8_t* __restrict__ Wq,
                                                                 const float* __restrict__ sw, int N, int K,

@@ -844,7 +844,8 @@ def backward_ckpt(layer: Layer, keep: Checkpoint, dY: torch.Tensor, ws: torch.Te
     """The layer's gradients from the checkpoint its forward kept: returns
     (dX or None, dA, dB, dbias or None).
 
-    ``act`` and ``z`` (the ``Checkpoint.z`` of the layer below) name the
+    In bf16, dX multiplies with the kernel Wq sw rounded to bf16, as ``backward``
+    does.  ``act`` and ``z`` (the ``Checkpoint.z`` of the layer below) name the
     activation that produced this layer's input: dX is taken back through it.
     ``add`` is added to dX (the gradient of a skip connection; it may be ``dX``
     itself).  ``ws``: ``ckpt_workspace``.  ``grads`` = (dA, dB, dbias or None)
