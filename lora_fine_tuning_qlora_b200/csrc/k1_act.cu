@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kSplitThreads) k1_split_kernel(const T* __rest
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(v[e]));
     }
-    const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));  // amax >= 0 or NaN, whose bits are above all
+    const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));  // amax >= 0 or NaN (above all)
     if (lane == 0) wmax[warp] = wm;
     // x . A needs no maximum: its loads go out before the barriers
     float acc[RP];

@@ -9,9 +9,9 @@
 // no memory latency (one buffer with the loads between two barriers: 34 us at
 // 64 x 784 x 128 in the backward, 13 CTAs on 8 steps of 16).  Fp32 products
 // and sums; for bf16 activations the kernel is rounded to bf16 first, as on
-// the tensor cores, so that dX follows one rule whatever N % 8 is.  Few tiles share their contraction over a cluster of S CTAs
-// (along x), whose partial tiles the first adds in rank order through
-// distributed shared memory.
+// the tensor cores, so that dX follows one rule whatever N % 8 is.  Few tiles
+// share their contraction over a cluster of S CTAs (along x), whose partial
+// tiles the first adds in rank order through distributed shared memory.
 #include "dx_common.cuh"
 #include "internal.h"
 #include "ptx.cuh"

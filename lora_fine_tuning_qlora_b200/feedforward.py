@@ -3,12 +3,13 @@ from 8-bit activations.
 
     Y = down(act(up(X))) + X          (the skip connection is optional)
 
-("Introduce QLoRA-like technique", GPT-2 and Gemma fine-tuning; keras-llm-light,
+("Introduce QLoRA-like technique", GPT-2 fine-tuning; keras-llm-light,
 "Block-wise gradient checkpointing", for keeping little between forward and
-backward.)  The activation, the residual and every checkpoint run in the
-GEMMs' epilogues; between the passes the block holds, per token, the codes of
-X and of act(Z) (K + N bytes), Z in 8 bits (1.125 N bytes) and a few floats,
-against 2 K + 4 N bytes of bf16 activations:
+backward.  A gated block, which multiplies two up projections, is not this one.)
+The activation, the residual and every checkpoint run in the GEMMs'
+epilogues; between the passes the block holds, per token, the codes of X and of
+act(Z) (K + N bytes), Z in 8 bits (1.125 N bytes) and a few floats, against 2 K
++ 4 N bytes of bf16 activations:
 
     forward   up:   Xq, sx, xA; H = act(Z), Z kept in 8 bits
               down: Hq, sh, hA; Y = H W2 + .. + X
