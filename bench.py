@@ -9,18 +9,20 @@ arithmetic-intensity argument for a 4096-wide layer).  With N GPUs (torchrun,
 one process per GPU) every rank runs its own 16384 tokens and the LoRA
 gradients are summed with one NCCL all-reduce per step (weak scaling).
 
-Beside the headline, the same JSON line carries a ``configs`` list: every
-layer of every benchmark workload (the single fp32 layer, the MNIST MLP
-stack, the GPT-2 base projections, the Gemma-2B projections at M = 512 and
-4096, the 4096-wide layer at M = 16 ... 16384), each with its step time, its
-TFLOP/s, the step roofline t_roof / t_measured, and every launch group's
-time and fraction of its own roofline.
+Beside the headline it times ``configs``: every layer of every benchmark
+workload (the single fp32 layer, the MNIST MLP stack, the GPT-2 base
+projections, the Gemma-2B projections at M = 512 and 4096, the 4096-wide layer
+at M = 16 ... 16384), each with its step time, its TFLOP/s, the step roofline
+t_roof / t_measured, and every launch group's time and fraction of its own
+roofline.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
-                    [--no-configs] [--only SUBSTRING]
+                    [--no-configs] [--only SUBSTRING] [--details FILE]
 
-Prints one JSON line (rank 0).  ``--impl reference`` times the CPU oracle on
-a bounded row sample of the headline layer, on the host cores.
+Prints one JSON line (rank 0) of at most LINE_BYTES, the headline's; a line per
+config goes to stderr, and ``--details`` writes everything as JSON.  ``--impl
+reference`` times the CPU oracle on a bounded row sample of the headline layer,
+on the host cores.
 """
 from __future__ import annotations
 
@@ -43,6 +45,7 @@ UNIT = "TFLOP/s"
 HEAD_M = 16384
 WORKLOAD = "dense4096_m16384_bf16_r4"
 L2_FLUSH_BYTES = 384 << 20
+LINE_BYTES = 2400  # of the printed line: what reads it keeps the last 3000 bytes of the output
 FALLBACK_PEAKS = {"hbm_gbs": 6650.0, "bf16_tflops": 1590.0, "bf16_tflops_sustained": 1400.0}
 # the kernel each launch group runs at the headline shape (other shapes may
 # take the single-CTA GEMMs or the register-resident quantizer)
@@ -57,6 +60,33 @@ PART_KERNELS = {
 
 def log(*a):
     print(*a, file=sys.stderr, flush=True)
+
+
+def rounded(v):
+    """v with every float at six significant digits."""
+    if isinstance(v, dict):
+        return {k: rounded(x) for k, x in v.items()}
+    if isinstance(v, (list, tuple)):
+        return [rounded(x) for x in v]
+    return float("%.6g" % v) if isinstance(v, float) else v
+
+
+def headline(full):
+    """The printed line of the full result: the headline with each launch
+    group's time; the rest is for --details."""
+    line = {k: v for k, v in full.items() if k not in ("configs", "merge", "kernels")}
+    line["step_roofline"] = {k: v for k, v in full["step_roofline"].items() if k != "rule"}
+    line["kernels_us"] = {k: v["us"] for k, v in full["kernels"].items()}
+    for extra in ("peaks", "kernels_us", "step_roofline", "cpu_baseline", None):
+        text = json.dumps(rounded(line))
+        if len(text) <= LINE_BYTES or extra is None:
+            return text
+        line.pop(extra)
+
+
+def config_row(c):
+    return "%-36s step %8.1f us  %7.1f TFLOP/s  %.3f of roofline" % (
+        c["workload"], c["step_us"], c["tflops"], c["roof_frac"])
 
 
 def load_peaks():
@@ -740,7 +770,12 @@ def run_ours(args):
                 "cpu_baseline": cpu, "clocks": clk,
                 "peaks": dict(peaks, source=peak_src),
                 "merge": merge, "configs": configs}
-        print(json.dumps(line), flush=True)
+        for c in configs or ():
+            log(config_row(c))
+        if args.details:
+            with open(args.details, "w") as f:
+                json.dump(line, f)
+        print(headline(line), flush=True)
     st.graph = None
     if world > 1:
         import torch.distributed as dist
@@ -757,6 +792,7 @@ def main(argv=None):
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-configs", action="store_true", help="headline only")
     ap.add_argument("--config-steps", type=int, default=10, help="timed steps per config layer")
+    ap.add_argument("--details", default="", help="also write the whole result, every config with it, to this file")
     ap.add_argument("--only", default="", help="time only the config layers whose name contains this")
     args = ap.parse_args(argv)
     if args.warmup < 3:
